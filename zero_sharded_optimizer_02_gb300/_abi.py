@@ -1,4 +1,5 @@
-"""ctypes binding of libzero.so: the C ABI of ``include/zero.h``, same names.
+"""ctypes binding of libzero.so: the C ABI of ``include/zero.h`` and
+``include/zero_train.h``, same names.
 
 Argument marshalling only: every step of the optimizer runs in the library's
 CUDA kernels.  Pointer arguments accept an int address or any object with a
@@ -55,7 +56,22 @@ class AdamW(C.Structure):
                 ("weight_decay", dbl), ("step", u64)]
 
 
+class Mat(C.Structure):
+    _fields_ = [("base", vp), ("rows", u64), ("cols", u64), ("pitch", u64), ("dtype", i32)]
+
+
+class Ids(C.Structure):
+    _fields_ = [("ids", vp), ("count", u64), ("bytes", u32)]
+
+
+class Act8(C.Structure):
+    _fields_ = [("q", vp), ("scale", vp), ("rows", u64), ("cols", u64), ("q_pitch", u64),
+                ("scale_pitch", u64)]
+
+
 _lib: C.CDLL | None = None
+
+_PM, _PI, _PA = C.POINTER(Mat), C.POINTER(Ids), C.POINTER(Act8)
 
 _SIGNATURES = {
     "zero_status_string": ([i32], C.c_char_p),
@@ -85,6 +101,16 @@ _SIGNATURES = {
     "zero_step_shard_unfused_static": ([C.POINTER(Grads), C.POINTER(Layout), C.POINTER(State),
                                         C.POINTER(State), vp, u64, u64, dbl, C.POINTER(AdamW),
                                         vp, vp], i32),
+    "zero_embed_lookup": ([_PM, _PI, C.c_float, _PM, vp, vp], i32),
+    "zero_embed_grad_workspace": ([u64, u64, u64], u64),
+    "zero_embed_grad": ([_PM, _PI, C.c_float, u32, _PM, vp, u64, vp, vp], i32),
+    "zero_norm_forward": ([_PM, _PM, vp, C.c_float, _PM, _PM, vp, _PA, vp], i32),
+    "zero_norm_backward_workspace": ([u64, u64], u64),
+    "zero_norm_backward": ([_PM, _PA, vp, vp, _PM, _PM, vp, u32, vp, u64, vp], i32),
+    "zero_act_pack": ([_PM, _PA, vp], i32),
+    "zero_act_unpack": ([_PA, _PM, vp], i32),
+    "zero_act_weight_grad_workspace": ([u64, u64, u64], u64),
+    "zero_act_weight_grad": ([_PM, _PA, vp, u32, _PM, vp, u64, vp], i32),
 }
 
 # Most contribution rows a gradient descriptor may name (include/zero.h).
@@ -397,3 +423,123 @@ def zero_step_shard_unfused_static(g: Grads, L: Layout, s_in: State, s_out: Stat
                                                 gathered_offset_elems, bucket_elems, loss_scale,
                                                 C.byref(h), _ptr(d_nonfinite), _stream(stream)),
            "zero_step_shard_unfused_static")
+
+
+# -- training operators (include/zero_train.h) ---------------------------------
+
+# Elements of a row that share one scale byte of an 8-bit checkpoint, and the
+# most columns the norm accepts (include/zero_train.h).
+ZERO_ACT8_BLOCK = 32
+ZERO_NORM_MAX_COLS = 32768
+
+
+def mat(t) -> Mat:
+    """Descriptor of a 2-D f16/bf16 torch tensor with contiguous rows (a view
+    of a larger buffer is fine).  It borrows t's memory: keep t alive."""
+    import torch
+    code = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16}.get(t.dtype)
+    if code is None or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("mat: a 2-D float16 or bfloat16 tensor with contiguous rows is needed, "
+                         f"not {tuple(t.shape)} {t.dtype} of strides {tuple(t.stride())}")
+    return Mat(t.data_ptr() or None, t.shape[0], t.shape[1], _row_pitch(t), code)
+
+
+def ids(t) -> Ids:
+    """Descriptor of a contiguous int32/int64 torch tensor of token numbers
+    (any shape; its elements in order).  It borrows t's memory."""
+    if t.element_size() not in (4, 8) or t.is_floating_point() or not t.is_contiguous():
+        raise ValueError(f"ids: a contiguous int32 or int64 tensor is needed, not {t.dtype} of "
+                         f"strides {tuple(t.stride())}")
+    return Ids(t.data_ptr() or None, t.numel(), t.element_size())
+
+
+def act8(q, scale) -> Act8:
+    """Descriptor of an 8-bit checkpoint: q int8 [rows, cols] and scale uint8
+    [rows, ceil(cols / 32)], rows contiguous.  It borrows their memory."""
+    import torch
+    if q.dtype != torch.int8 or scale.dtype != torch.uint8 or q.dim() != 2 or scale.dim() != 2 \
+            or (q.shape[1] > 1 and q.stride(1) != 1) \
+            or (scale.shape[1] > 1 and scale.stride(1) != 1) \
+            or tuple(scale.shape) != (q.shape[0], -(-q.shape[1] // ZERO_ACT8_BLOCK)):
+        raise ValueError("act8: q int8 [rows, cols] and scale uint8 [rows, ceil(cols / 32)] with "
+                         f"contiguous rows are needed, not {tuple(q.shape)} {q.dtype} and "
+                         f"{tuple(scale.shape)} {scale.dtype}")
+    return Act8(q.data_ptr() or None, scale.data_ptr() or None, q.shape[0], q.shape[1],
+                _row_pitch(q), _row_pitch(scale))
+
+
+def act8_empty(rows: int, cols: int, device="cuda"):
+    """Memory for the checkpoint of a [rows, cols] matrix: (q, scale)."""
+    import torch
+    q = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.int8, device=device)[:, :cols]
+    return q, torch.empty(rows, -(-cols // ZERO_ACT8_BLOCK), dtype=torch.uint8, device=device)
+
+
+def _row_pitch(t) -> int:
+    """Elements between a 2-D tensor's rows (torch may give any stride to a
+    dimension of one element)."""
+    if t.shape[0] > 1:
+        return t.stride(0)   # 0 for a broadcast row: refused (pitch < cols)
+    return -(-t.shape[1] // 16) * 16
+
+
+def _ref(s):
+    return None if s is None else C.byref(s)
+
+
+def zero_embed_lookup(table: Mat, token_ids: Ids, scale: float, out: Mat, d_bad=None,
+                      stream=None) -> None:
+    _check(lib().zero_embed_lookup(_ref(table), _ref(token_ids), scale, _ref(out), _ptr(d_bad),
+                                   _stream(stream)), "zero_embed_lookup")
+
+
+def zero_embed_grad_workspace(tokens: int, vocab: int, dim: int) -> int:
+    return int(lib().zero_embed_grad_workspace(tokens, vocab, dim))
+
+
+def zero_embed_grad(d_out: Mat, token_ids: Ids, scale: float, accumulate: bool, d_table: Mat,
+                    workspace, workspace_bytes: int, d_bad=None, stream=None) -> None:
+    _check(lib().zero_embed_grad(_ref(d_out), _ref(token_ids), scale, int(accumulate),
+                                 _ref(d_table), _ptr(workspace), workspace_bytes, _ptr(d_bad),
+                                 _stream(stream)), "zero_embed_grad")
+
+
+def zero_norm_forward(x: Mat, residual: Mat | None, gain, eps: float, h: Mat | None,
+                      y: Mat | None, rstd=None, checkpoint: Act8 | None = None,
+                      stream=None) -> None:
+    _check(lib().zero_norm_forward(_ref(x), _ref(residual), _ptr(gain), eps, _ref(h), _ref(y),
+                                   _ptr(rstd), _ref(checkpoint), _stream(stream)),
+           "zero_norm_forward")
+
+
+def zero_norm_backward_workspace(rows: int, cols: int) -> int:
+    return int(lib().zero_norm_backward_workspace(rows, cols))
+
+
+def zero_norm_backward(dy: Mat, checkpoint: Act8, rstd, gain, d_residual: Mat | None, dx: Mat,
+                       d_gain, accumulate: bool, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    _check(lib().zero_norm_backward(_ref(dy), _ref(checkpoint), _ptr(rstd), _ptr(gain),
+                                    _ref(d_residual), _ref(dx), _ptr(d_gain), int(accumulate),
+                                    _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_norm_backward")
+
+
+def zero_act_pack(x: Mat, out: Act8, stream=None) -> None:
+    _check(lib().zero_act_pack(_ref(x), _ref(out), _stream(stream)), "zero_act_pack")
+
+
+def zero_act_unpack(checkpoint: Act8, out: Mat, stream=None) -> None:
+    _check(lib().zero_act_unpack(_ref(checkpoint), _ref(out), _stream(stream)),
+           "zero_act_unpack")
+
+
+def zero_act_weight_grad_workspace(tokens: int, outs: int, ins: int) -> int:
+    return int(lib().zero_act_weight_grad_workspace(tokens, outs, ins))
+
+
+def zero_act_weight_grad(dy: Mat, x: Act8, gain, accumulate: bool, dw: Mat, workspace,
+                         workspace_bytes: int, stream=None) -> None:
+    _check(lib().zero_act_weight_grad(_ref(dy), _ref(x), _ptr(gain), int(accumulate), _ref(dw),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_act_weight_grad")

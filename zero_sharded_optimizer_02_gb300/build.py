@@ -1,6 +1,6 @@
 """Builds libzero.so in-tree: the CUDA kernels for sm_103a plus the host C++.
 
-Two translation units are compiled in parallel and linked with the static
+The translation units are compiled in parallel and linked with the static
 CUDA runtime, so the library loads without a GPU (symbol checks) and needs no
 library path at run time.
 """
@@ -26,6 +26,14 @@ SOURCES = {
                          "-fPIC", "-Xptxas", "-v", "-I", INCLUDE, "-c"],
     "zero_gather.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
                        "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_embed.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                      "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_norm.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                     "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_wgrad.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                      "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_train_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I",
+                            INCLUDE, "-c"],
     "zero_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE,
                       "-c"],
     "zero_checkpoint.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-pthread", "-Wall",
@@ -77,7 +85,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         force = True
         with open(stamp, "w") as f:
             f.write(key)
-    headers = [os.path.join(INCLUDE, "zero.h"), os.path.join(csrc, "zero_internal.h"),
+    headers = [os.path.join(INCLUDE, "zero.h"), os.path.join(INCLUDE, "zero_train.h"),
+               os.path.join(csrc, "zero_internal.h"), os.path.join(csrc, "zero_train_internal.h"),
+               os.path.join(csrc, "zero_train_device.cuh"),
                os.path.join(csrc, "zero_device.cuh"), os.path.join(csrc, "zero_ring.cuh"),
                os.path.join(csrc, "zero_small.cuh")]
     objs, procs = [], []
