@@ -2,6 +2,7 @@
 // 16-bit vectors with ragged ends, and the 8-bit checkpoint's arithmetic.
 #pragma once
 
+#include <atomic>
 #include <utility>
 
 #include "zero_device.cuh"
@@ -58,6 +59,22 @@ inline int sm_count()
         return 0;
     }
     return n;
+}
+
+// Lets `fn` use `bytes` of dynamic shared memory (once per device; `done` has
+// a bit per device).
+template <typename F>
+void allow_smem(F* fn, size_t bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        dev = 64;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit))
+        return;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+            cudaSuccess && bit)
+        done.fetch_or(bit, std::memory_order_relaxed);
 }
 
 // -- 16-bit vectors of 8 elements ---------------------------------------------
