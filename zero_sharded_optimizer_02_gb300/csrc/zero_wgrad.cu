@@ -8,11 +8,12 @@
 // outputs: a CTA holds 128 of the inputs (the rows of its half of the
 // accumulator) and 128 of the outputs.
 //   - dy goes from global memory to shared memory by TMA;
-//   - the checkpoint's bytes go through registers: eight warps load 16
-//     elements of a token at a time, turn them into 16-bit values (exact: a
-//     whole number of 7 bits and sign times a power of two) and store them
-//     where the tensor cores read them.  The 16-bit matrix that a separate
-//     unpack would write and read back never exists;
+//   - the checkpoint's bytes go to shared memory by TMA too, their scale bytes to
+//     registers.  Two groups of four warps take the steps in turn: each turns
+//     16 elements of a token at a time into 16-bit values (exact: a whole number
+//     of 7 bits and sign times a power of two) and stores them where the tensor
+//     cores read them.  The 16-bit matrix that a
+//     separate unpack would write and read back never exists;
 //   - one thread of the pair issues the products; four warps of each CTA drain
 //     finished accumulators (two of 256 columns in tensor memory) while the
 //     next tile is summed.
@@ -35,22 +36,32 @@ constexpr int kPairs = 76;         // CTA pairs of one wave: 152 SMs
 constexpr int kTileI = 256;        // inputs of a pair's tile, 128 a CTA
 constexpr int kTileO = 256;        // outputs of a pair's tile
 constexpr int kStepT = 64;         // tokens of a stage
-constexpr int kStages = 6;
+constexpr int kXStages = 4;        // converted inputs
+constexpr int kYStages = 6;        // dy
+constexpr int kRawStages = 6;      // the checkpoint's bytes
 constexpr int kHalf = 128;         // inputs, and outputs, that one CTA loads
 constexpr int kOperandBytes = kHalf * kStepT * 2;            // 16 KB
-constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kGroupBytes = 64 * kStepT * 2;                 // 64 elements of every token
-constexpr int kBarriers = 3 * kStages + 4;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBarriers * 8 + 16;
+constexpr int kRawBytes = kHalf * kStepT;                    // 8 KB
+constexpr int kEpilogueWarps = 4;
+constexpr int kTurnPitch = 32 * 2 + 16;                      // bytes of a row of a turned 32 x 32 tile
+constexpr int kTurnBytes = 32 * kTurnPitch;
+constexpr int kYAt = kXStages * kOperandBytes;
+constexpr int kRawAt = kYAt + kYStages * kOperandBytes;
+constexpr int kTurnAt = kRawAt + kRawStages * kRawBytes;
+constexpr int kBarrierAt = kTurnAt + kEpilogueWarps * kTurnBytes;
+constexpr int kBarriers = 2 * kXStages + 2 * kYStages + 2 * kRawStages + 4;
+constexpr int kSmemBytes = 1024 + kBarrierAt + kBarriers * 8 + 16;
 static_assert(kSmemBytes <= 227 * 1024, "stages exceed shared memory");
+constexpr int kScalesAhead = 2;    // own steps whose scale bytes a converting warp loads ahead
 constexpr int kTmemCols = 512;     // two accumulators of 256 fp32 columns
 
-constexpr int kConvertWarps = 8;
-constexpr int kEpilogueWarps = 4;
-// warp 0: copies; warp 1: products; warps 2..9: conversion; warps 10..13: epilogue
-constexpr int kFirstEpilogueWarp = 2 + kConvertWarps;
-constexpr int kThreads = 32 * (2 + kConvertWarps + kEpilogueWarps);
-constexpr int kAhead = 3;          // stages a converting thread loads ahead, in registers
+constexpr int kGroups = 2;         // converting groups
+constexpr int kGroupWarps = 4;
+// warp 0: copies of dy; 1: products; 2..9: conversion; 10..13: epilogue; 14: copies of the checkpoint
+constexpr int kFirstEpilogueWarp = 2 + kGroups * kGroupWarps;
+constexpr int kRawWarp = kFirstEpilogueWarp + kEpilogueWarps;
+constexpr int kThreads = 32 * (kRawWarp + 1);
 
 constexpr uint64_t kWaitNs = 4ull * 1000 * 1000 * 1000;
 
@@ -168,9 +179,14 @@ __device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank)
     return r;
 }
 
+// Arrives on a barrier of the pair's other (or this) CTA.  Release at CTA
+// scope: what the arrival announces is this CTA's shared and tensor memory as
+// the tensor cores see it, which the writer's proxy fence (or tcgen05 fence)
+// has ordered already.  A release at cluster scope waits for the whole memory
+// system and held every token step to about 1,200 clocks.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
@@ -186,20 +202,36 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
 }
 
 // Waits for the phase of parity `parity`; false if that took over kWaitNs or
-// another wait of this CTA has run out (`failed`, shared memory).
+// another wait of this CTA has run out (`failed`, shared memory).  The clock
+// is first read after 1,024 tries: reading it before the first retry added
+// about a microsecond to every wait that had to wait at all.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* failed)
 {
-    if (try_wait_cluster(bar, parity))
-        return true;
-    const uint64_t t0 = global_ns();
+    uint64_t t0 = 0;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
-        if (try_wait_cluster(bar, parity))
+        if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
             return true;
-        if ((i & 63) == 63 && (*failed || global_ns() - t0 > kWaitNs))
-            break;
+        if ((i & 1023) == 1023) {
+            const uint64_t t = global_ns();
+            if (!t0)
+                t0 = t;
+            if (*failed || t - t0 > kWaitNs)
+                break;
+        }
     }
     *failed = 1;
     return false;
+}
+
+// A box of a matrix into this CTA's shared memory at dst; its bytes count on
+// this CTA's barrier `bar`.
+__device__ __forceinline__ void tma_box_own(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
 }
 
 // A 64 x 64 box of a 16-bit matrix into this CTA's shared memory at dst; its
@@ -341,38 +373,41 @@ struct WgradArgs {
     uint64_t q_pitch, scale_pitch, dw_pitch;
     uint64_t tokens, outs, ins;
     uint32_t add;
+    uint32_t dw_vec;     // dw's rows start on 16-byte boundaries
     Plan plan;
 };
 
-// 16 elements of one token on their way through registers.
+// The scale bytes of 128 inputs from block b on, of token t, as a word (a
+// block or token that does not exist gets the step 1).  Rows need no alignment:
+// away from the ends of the array the word is cut out of the two aligned words
+// around it, which lie in this and the neighbouring rows.
+__device__ __forceinline__ uint32_t load_scales(const WgradArgs& a, uint64_t t, uint32_t b, uint32_t blocks)
+{
+    if (t >= a.tokens)
+        return 0x7F7F7F7Fu;
+    const uint8_t* p = a.scale + t * a.scale_pitch + b;
+    if (b + 4 <= blocks) {
+        const uint32_t phase = (uint32_t)(uintptr_t)p & 3;
+        if (phase == 0)
+            return __ldg(reinterpret_cast<const uint32_t*>(p));
+        if (a.scale_pitch >= 4 && t > 0 && t + 1 < a.tokens) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p - phase);
+            return __funnelshift_r(__ldg(w), __ldg(w + 1), phase * 8);
+        }
+    }
+    uint32_t w = 0x7F7F7F7Fu;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+        if (b + i < blocks)
+            w = (w & ~(0xFFu << (8 * i))) | (uint32_t)p[i] << (8 * i);
+    return w;
+}
+
+// 16 elements of one token.
 struct Chunk {
     uint4 q;
     uint32_t s;
 };
-
-__device__ __forceinline__ Chunk load_chunk(const WgradArgs& a, uint64_t t, uint64_t c)
-{
-    Chunk k;
-    k.q = make_uint4(0, 0, 0, 0);
-    k.s = 127;
-    if (t < a.tokens && c < a.ins) {
-        const int8_t* p = a.q + t * a.q_pitch + c;
-        if (c + 16 <= a.ins) {
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(k.q.x), "=r"(k.q.y), "=r"(k.q.z), "=r"(k.q.w)
-                         : "l"(p));
-        } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < a.ins)
-                    w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
-            k.q = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        k.s = a.scale[t * a.scale_pitch + c / ZERO_ACT8_BLOCK];
-    }
-    return k;
-}
 
 template <int DT>
 __device__ __forceinline__ void convert_chunk(const Chunk& k, uint4& lo, uint4& hi)
@@ -397,22 +432,26 @@ __device__ __forceinline__ void store_shared16(uint32_t addr, uint4 v)
                  : "memory");
 }
 
-// Where a converting thread is in the pair's sequence of token steps.
-struct Cursor {
-    uint32_t u, k, k1;
-    uint64_t c;         // its first input
-};
+__device__ __forceinline__ uint4 load_shared16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    k_weight_grad(const __grid_constant__ CUtensorMap dy, const __grid_constant__ WgradArgs a)
+    k_weight_grad(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap q,
+                  const __grid_constant__ WgradArgs a)
 {
     extern __shared__ unsigned char raw[];
     pdl_entry();
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
-    const uint32_t bars = base + kStages * kStageBytes;
-    const uint32_t full_x = bars, full_y = bars + 8 * kStages, empty = bars + 16 * kStages;
-    const uint32_t tmem_full = bars + 24 * kStages, tmem_empty = tmem_full + 16;
+    const uint32_t bars = base + kBarrierAt;
+    const uint32_t full_x = bars, empty_x = full_x + 8 * kXStages;
+    const uint32_t full_y = empty_x + 8 * kXStages, empty_y = full_y + 8 * kYStages;
+    const uint32_t raw_full = empty_y + 8 * kYStages, raw_empty = raw_full + 8 * kRawStages;
+    const uint32_t tmem_full = raw_empty + 8 * kRawStages, tmem_empty = tmem_full + 16;
     uint32_t* words = reinterpret_cast<uint32_t*>(raw + (bars + 8 * kBarriers - smem_u32(raw)));
     volatile uint32_t* failed = words + 1;
     const uint32_t rank = cluster_rank();
@@ -421,10 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
     if (threadIdx.x == 0) {
         *failed = 0;
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full_x + 8 * s, 2 * kConvertWarps);
+        for (int s = 0; s < kXStages; ++s) {
+            mbar_init(full_x + 8 * s, 2 * kGroupWarps);
+            mbar_init(empty_x + 8 * s, 1);
+        }
+        for (int s = 0; s < kYStages; ++s) {
             mbar_init(full_y + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);
+            mbar_init(empty_y + 8 * s, 1);
+        }
+        for (int s = 0; s < kRawStages; ++s) {
+            mbar_init(raw_full + 8 * s, 1);
+            mbar_init(raw_empty + 8 * s, kGroupWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tmem_full + 8 * b, 1);
@@ -444,6 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(words);
 
+    uint32_t total = 0;   // token steps of this pair
+    for (uint32_t u = pair; u < a.plan.units; u += pairs) {
+        const Unit t = unit_at(a.plan, u);
+        total += t.k1 - t.k0;
+    }
+
     if (warp == 0) {
         if (lane == 0) {   // copies of dy
             uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
@@ -452,19 +504,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Unit t = unit_at(a.plan, u);
                 const int x = (int)(t.to * kTileO + rank * kHalf);
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    if (!wait_phase(empty + 8 * stage, phase ^ 1, failed)) {
+                    if (!wait_phase(empty_y + 8 * stage, phase ^ 1, failed)) {
                         ok = false;
                         break;
                     }
                     if (rank == 0)
                         mbar_arrive_expect_tx(full_y + 8 * stage, 2 * kOperandBytes);
                     const uint32_t bar = map_shared(full_y + 8 * stage, 0);
-                    const uint32_t dst = base + stage * kStageBytes + kOperandBytes;
+                    const uint32_t dst = base + kYAt + stage * kOperandBytes;
                     tma_box(dst, &dy, x, (int)(k * kStepT), bar);
                     tma_box(dst + kGroupBytes, &dy, x + 64, (int)(k * kStepT), bar);
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | phase << stage;
-                    if (++stage == kStages) {
+                    if (++stage == kYStages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -473,37 +525,42 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // The pair does not end under its own copies: both CTAs' bytes count on
             // the first one's barriers, and the other waits for it below.
             if (rank == 0)
-                for (uint32_t s = 0; s < kStages; ++s)
+                for (uint32_t s = 0; s < kYStages; ++s)
                     if (armed >> s & 1)
                         mbar_wait(full_y + 8 * s, armed_phase >> s & 1, kWaitNs);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {   // products
-            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            uint32_t xs = 0, x_phase = 0, ys = 0, y_phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (uint32_t u = pair; u < a.plan.units && ok; u += pairs) {
                 const Unit t = unit_at(a.plan, u);
-                ok = wait_phase(tmem_empty + 8 * buf, buf_phase ^ 1, failed);
+                ok = wait_phase<true>(tmem_empty + 8 * buf, buf_phase ^ 1, failed);
                 if (!ok)
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tmem + buf * kTileO;
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    ok = wait_phase(full_y + 8 * stage, phase, failed) &&
-                         wait_phase(full_x + 8 * stage, phase, failed);
+                    ok = wait_phase(full_y + 8 * ys, y_phase, failed) &&
+                         wait_phase<true>(full_x + 8 * xs, x_phase, failed);
                     if (!ok)
                         break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t xd = operand_desc(base + stage * kStageBytes);
-                    const uint64_t yd = operand_desc(base + stage * kStageBytes + kOperandBytes);
+                    const uint64_t xd = operand_desc(base + xs * kOperandBytes);
+                    const uint64_t yd = operand_desc(base + kYAt + ys * kOperandBytes);
 #pragma unroll
                     for (int j = 0; j < kStepT / 16; ++j)   // 16 tokens: 2048 bytes further
                         mma_pair(acc, xd + j * (2048 >> 4), yd + j * (2048 >> 4), instr_desc<DT>(),
                                  k > t.k0 || j > 0);
-                    commit_pair(empty + 8 * stage);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                    commit_pair(empty_x + 8 * xs);
+                    commit_pair(empty_y + 8 * ys);
+                    if (++xs == kXStages) {
+                        xs = 0;
+                        x_phase ^= 1;
+                    }
+                    if (++ys == kYStages) {
+                        ys = 0;
+                        y_phase ^= 1;
                     }
                 }
                 if (!ok)
@@ -514,75 +571,124 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
     } else if (warp < kFirstEpilogueWarp) {
-        // conversion: this thread's 16 inputs of tokens tok and tok + 32 of every step.
-        // Lanes 0..3 and 4..7 store tokens of different parity, whose swizzles
-        // keep the eight 16-byte stores of a quarter warp on different banks.
-        const uint32_t w = warp - 2, group = w / 4;
-        const uint32_t tok = (w % 4) * 8 + lane / 4;
-        const uint32_t col = group * 64 + (lane % 4) * 16;
-        const uint32_t row = group * kGroupBytes + tok * 128;
-        const uint32_t c0 = ((lane % 4) * 2 ^ (tok & 7)) * 16, c1 = ((lane % 4) * 2 + 1 ^ (tok & 7)) * 16;
-        uint32_t total = 0;
-        for (uint32_t u = pair; u < a.plan.units; u += pairs) {
-            const Unit t = unit_at(a.plan, u);
-            total += t.k1 - t.k0;
-        }
-        Cursor at;
-        at.u = pair;
-        at.k = at.k1 = 0;
-        at.c = 0;
-        Chunk ahead[kAhead][2];
-        auto fetch = [&](Chunk (&k)[2]) {
-            if (at.k == at.k1) {
-                const Unit t = unit_at(a.plan, at.u);
-                at.k = t.k0;
-                at.k1 = t.k1;
-                at.c = (uint64_t)t.ti * kTileI + rank * kHalf + col;
-                at.u += pairs;
+        // conversion: group g takes steps g, g + 2, ...  A thread takes 16 inputs of
+        // either half at tokens tok and tok + 32.  Lanes 0..3 and 4..7 of a quarter
+        // warp take tokens that differ in bits 0 and 2, whose swizzles keep its
+        // 16-byte loads, and its stores, on different banks.
+        const uint32_t group = (warp - 2) / kGroupWarps;
+        const uint32_t p = lane / 4, j = lane % 4;
+        const uint32_t tok = (warp - 2) % kGroupWarps * 8 + (p / 2 ^ (p & 1) * 5);
+        const uint32_t sw = tok & 7;
+        const uint32_t from0 = tok * 128 + (j ^ sw) * 16, from1 = tok * 128 + (4 + j ^ sw) * 16;
+        const uint32_t to0 = tok * 128 + (2 * j ^ sw) * 16, to1 = tok * 128 + (2 * j + 1 ^ sw) * 16;
+        // the step that this thread's next scale bytes belong to
+        const uint32_t blocks = (uint32_t)((a.ins + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK);
+        uint32_t at_u = pair, at_k = 0, at_k1 = 0, at_b = 0, skip = group;
+        uint32_t sc[kScalesAhead][2];
+        auto fetch = [&](uint32_t (&w)[2]) {
+            at_k += skip;
+            while (at_k >= at_k1) {
+                const Unit t = unit_at(a.plan, at_u);
+                at_k = t.k0 + (at_k - at_k1);
+                at_k1 = t.k1;
+                at_b = (t.ti * kTileI + rank * kHalf) / ZERO_ACT8_BLOCK;
+                at_u += pairs;
             }
-            const uint64_t t = (uint64_t)at.k * kStepT + tok;
-            k[0] = load_chunk(a, t, at.c);
-            k[1] = load_chunk(a, t + 32, at.c);
-            ++at.k;
+            const uint64_t t = (uint64_t)at_k * kStepT + tok;
+            w[0] = load_scales(a, t, at_b, blocks);
+            w[1] = load_scales(a, t + 32, at_b, blocks);
+            skip = kGroups;
         };
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (j < total)
-                fetch(ahead[j]);
-        uint32_t stage = 0, phase = 0;
+        for (int i = 0; i < kScalesAhead; ++i)
+            if (group + i * kGroups < total)
+                fetch(sc[i]);
+        uint32_t stage = group, phase = 0, rstage = group, rphase = 0;
+        static_assert(kGroups <= kXStages && kGroups <= kRawStages, "a group's first stage");
         bool ok = true;   // the same in the whole warp
-        for (uint32_t n0 = 0; n0 < total && ok; n0 += kAhead)
+        for (uint32_t n0 = group; n0 < total && ok; n0 += kGroups * kScalesAhead)
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const uint32_t n = n0 + j;
+            for (int h = 0; h < kScalesAhead; ++h) {
+                const uint32_t n = n0 + h * kGroups;
                 if (n >= total || !ok)
                     break;
-                uint4 v[4];
-                convert_chunk<DT>(ahead[j][0], v[0], v[1]);
-                convert_chunk<DT>(ahead[j][1], v[2], v[3]);
-                if (n + kAhead < total)
-                    fetch(ahead[j]);
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(empty + 8 * stage, phase ^ 1, failed));
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(raw_full + 8 * rstage, rphase, failed));
                 if (!ok)
                     break;
-                const uint32_t dst = base + stage * kStageBytes + row;
-                store_shared16(dst + c0, v[0]);
-                store_shared16(dst + c1, v[1]);
-                store_shared16(dst + 32 * 128 + c0, v[2]);
-                store_shared16(dst + 32 * 128 + c1, v[3]);
+                const uint32_t src = base + kRawAt + rstage * kRawBytes;
+                Chunk k[4];
+                k[0].q = load_shared16(src + from0);
+                k[1].q = load_shared16(src + from1);
+                k[2].q = load_shared16(src + 32 * 128 + from0);
+                k[3].q = load_shared16(src + 32 * 128 + from1);
+                k[0].s = sc[h][0] >> (j / 2 * 8) & 0xFF;
+                k[1].s = sc[h][0] >> (16 + j / 2 * 8) & 0xFF;
+                k[2].s = sc[h][1] >> (j / 2 * 8) & 0xFF;
+                k[3].s = sc[h][1] >> (16 + j / 2 * 8) & 0xFF;
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    convert_chunk<DT>(k[i], v[2 * i], v[2 * i + 1]);
+                if (n + kGroups * kScalesAhead < total)
+                    fetch(sc[h]);
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(empty_x + 8 * stage, phase ^ 1, failed));
+                if (!ok)
+                    break;
+                const uint32_t dst = base + stage * kOperandBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // half i % 2, tokens + 32 (i / 2)
+                    store_shared16(dst + i % 2 * kGroupBytes + i / 2 * 32 * 128 + to0, v[2 * i]);
+                    store_shared16(dst + i % 2 * kGroupBytes + i / 2 * 32 * 128 + to1, v[2 * i + 1]);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
                     arrive_cluster(map_shared(full_x + 8 * stage, 0));
-                if (++stage == kStages) {
-                    stage = 0;
+                    mbar_arrive(raw_empty + 8 * rstage);
+                }
+                if ((stage += kGroups) >= kXStages) {
+                    stage -= kXStages;
                     phase ^= 1;
                 }
+                if ((rstage += kGroups) >= kRawStages) {
+                    rstage -= kRawStages;
+                    rphase ^= 1;
+                }
             }
+    } else if (warp == kRawWarp) {
+        if (lane == 0) {   // copies of the checkpoint
+            uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
+            bool ok = true;
+            for (uint32_t u = pair; u < a.plan.units && ok; u += pairs) {
+                const Unit t = unit_at(a.plan, u);
+                const int x = (int)(t.ti * kTileI + rank * kHalf);
+                for (uint32_t k = t.k0; k < t.k1; ++k) {
+                    ok = wait_phase(raw_empty + 8 * stage, phase ^ 1, failed);
+                    if (!ok)
+                        break;
+                    mbar_arrive_expect_tx(raw_full + 8 * stage, kRawBytes);
+                    tma_box_own(base + kRawAt + stage * kRawBytes, &q, x, (int)(k * kStepT),
+                                raw_full + 8 * stage);
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | phase << stage;
+                    if (++stage == kRawStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            for (uint32_t s = 0; s < kRawStages; ++s)   // as for dy's
+                if (armed >> s & 1)
+                    mbar_wait(raw_full + 8 * s, armed_phase >> s & 1, kWaitNs);
+        }
     } else {
         // epilogue: warp w of the CTA may read the tensor memory lanes 32 (w mod 4) .. + 31;
         // a lane is an input, a column an output
         const uint32_t quarter = warp % 4;
+        // A tile of 32 inputs x 32 outputs is turned in shared memory, so that a
+        // row of dw is stored 64 bytes at a time by four lanes.
+        const uint32_t turn = base + kTurnAt + quarter * kTurnBytes;
+        const uint32_t mine = turn + lane * 2, line = turn + lane / 4 * kTurnPitch + lane % 4 * 16;
         uint32_t buf = 0, buf_phase = 0;
         for (uint32_t u = pair; u < a.plan.units; u += pairs) {
             const Unit t = unit_at(a.plan, u);
@@ -604,17 +710,48 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         p[(uint32_t)j * kTileI] = __uint_as_float(v[j]);
+                } else if (a.dw_vec && i - lane + 32 <= a.ins) {
+                    uint16_t* p = a.dw + (o0 + c + lane / 4) * a.dw_pitch + (i - lane) + lane % 4 * 8;
+                    __syncwarp();   // the previous tile has been read
+                    if (a.add) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (o0 + c + j * 8 + lane / 4 < a.outs)
+                                w[j] = *reinterpret_cast<const uint4*>(p + j * 8 * a.dw_pitch);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            store_shared16(line + j * 8 * kTurnPitch, w[j]);
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float x = __uint_as_float(v[j]) * gain;
+                        if (a.add) {
+                            uint16_t b;
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(mine + j * kTurnPitch));
+                            x += widen1<DT>(b);
+                        }
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(mine + j * kTurnPitch), "h"(narrow1<DT>(x))
+                                     : "memory");
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (o0 + c + j * 8 + lane / 4 < a.outs)
+                            *reinterpret_cast<uint4*>(p + j * 8 * a.dw_pitch) =
+                                load_shared16(line + j * 8 * kTurnPitch);
                 } else if (i < a.ins) {
                     uint16_t* p = a.dw + (o0 + c) * a.dw_pitch + i;
                     const uint32_t n = o0 + c < a.outs ? (uint32_t)min((uint64_t)32, a.outs - o0 - c) : 0;
+                    float old[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j < n) {
-                            float x = __uint_as_float(v[j]) * gain;
-                            if (a.add)
-                                x += widen1<DT>(p[j * a.dw_pitch]);
-                            p[j * a.dw_pitch] = narrow1<DT>(x);
-                        }
+                        old[j] = a.add && j < n ? widen1<DT>(p[j * a.dw_pitch]) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < n)
+                            p[j * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[j]) * gain + old[j]);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -699,13 +836,26 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
+// Map of a matrix for boxes of kStepT rows x `box` columns (128 bytes wide) in
+// the 128-byte swizzle; what lies outside the matrix reads as zero.
+bool encode_rows(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t cols,
+                 uint64_t rows, uint64_t pitch_bytes, uint32_t box)
+{
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {pitch_bytes};
+    const cuuint32_t boxes[2] = {box, kStepT}, unit[2] = {1, 1};
+    return encode(map, type, 2, base, dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DT>
-cudaError_t launch_products(const CUtensorMap& map, const WgradArgs& a, bool vec, void* stream)
+cudaError_t launch_products(const CUtensorMap& dy, const CUtensorMap& q, const WgradArgs& a, bool vec, void* stream)
 {
     static std::atomic<uint64_t> allowed{0};
     allow_smem(k_weight_grad<DT>, kSmemBytes, allowed);
     const uint32_t pairs = a.plan.units < kPairs ? a.plan.units : kPairs;
-    cudaError_t e = launch_train(k_weight_grad<DT>, dim3(2 * pairs), kThreads, kSmemBytes, 1, stream, map, a);
+    cudaError_t e = launch_train(k_weight_grad<DT>, dim3(2 * pairs), kThreads, kSmemBytes, 1, stream, dy, q, a);
     if (e == cudaSuccess && a.plan.splits > 1) {
         const uint32_t cut = a.plan.tiles_i * a.plan.tiles_o - a.plan.full;
         e = launch_train(vec ? k_weight_join<DT, true> : k_weight_join<DT, false>, dim3(cut * kJoinCtas),
@@ -747,7 +897,8 @@ extern "C" zero_status_t zero_act_weight_grad(const zero_mat_t* dy, const zero_a
     if (dw->rows == 0 || dw->cols == 0 || (dy->rows == 0 && accumulate))
         return ZERO_OK;
     Plan plan;
-    if (!make_plan(dy->rows, dy->cols, x->cols, &plan) || dy->pitch >= (1ull << 38))
+    if (!make_plan(dy->rows, dy->cols, x->cols, &plan) || dy->pitch >= (1ull << 38) ||
+        x->q_pitch >= (1ull << 39))
         return ZERO_ERR_UNSUPPORTED;
     const uint64_t need = plan_workspace(plan);
     if (need && (!workspace || workspace_bytes < need))
@@ -790,16 +941,14 @@ extern "C" zero_status_t zero_act_weight_grad(const zero_mat_t* dy, const zero_a
     const EncodeTiled encode = encode_tiled();
     if (!encode)
         return ZERO_ERR_CUDA;
-    CUtensorMap map;
     const bool f16 = dy->dtype == ZERO_F16;
-    const cuuint64_t dims[2] = {dy->cols, dy->rows};
-    const cuuint64_t strides[1] = {2 * dy->pitch};
-    const cuuint32_t box[2] = {64, kStepT}, unit[2] = {1, 1};
-    if (encode(&map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy->base,
-               dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    CUtensorMap ymap, qmap;
+    if (!encode_rows(encode, &ymap, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     dy->base, dy->cols, dy->rows, 2 * dy->pitch, 64) ||
+        !encode_rows(encode, &qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->q, x->cols, x->rows, x->q_pitch, kHalf))
         return ZERO_ERR_CUDA;
     const bool vec = (uintptr_t)dw->base % 16 == 0 && dw->pitch % 8 == 0;
-    return train_status(f16 ? launch_products<ZERO_F16>(map, a, vec, stream)
-                            : launch_products<ZERO_BF16>(map, a, vec, stream));
+    a.dw_vec = vec;
+    return train_status(f16 ? launch_products<ZERO_F16>(ymap, qmap, a, vec, stream)
+                            : launch_products<ZERO_BF16>(ymap, qmap, a, vec, stream));
 }
