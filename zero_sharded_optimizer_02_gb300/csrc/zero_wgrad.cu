@@ -8,11 +8,11 @@
 // outputs: a CTA holds 128 of the inputs (the rows of its half of the
 // accumulator) and 128 of the outputs.
 //   - dy goes from global memory to shared memory by TMA;
-//   - the checkpoint's bytes go to shared memory by TMA too, their scale bytes to
-//     registers.  Two groups of four warps take the steps in turn: each turns
-//     16 elements of a token at a time into 16-bit values (exact: a whole number
-//     of 7 bits and sign times a power of two) and stores them where the tensor
-//     cores read them.  The 16-bit matrix that a
+//   - the checkpoint's bytes go to shared memory by TMA too; three pairs of warps
+//     load its scale bytes and leave the steps beside them.  Three groups of four
+//     warps take the token steps in turn: each turns 16 elements of a token at a time
+//     into 16-bit values (exact: a whole number of 7 bits and sign times a power
+//     of two) and stores them where the tensor cores read them.  The 16-bit matrix that a
 //     separate unpack would write and read back never exists;
 //   - one thread of the pair issues the products; four warps of each CTA drain
 //     finished accumulators (two of 256 columns in tensor memory) while the
@@ -36,32 +36,61 @@ constexpr int kPairs = 76;         // CTA pairs of one wave: 152 SMs
 constexpr int kTileI = 256;        // inputs of a pair's tile, 128 a CTA
 constexpr int kTileO = 256;        // outputs of a pair's tile
 constexpr int kStepT = 64;         // tokens of a stage
-constexpr int kXStages = 4;        // converted inputs
-constexpr int kYStages = 6;        // dy
+constexpr int kStages = 5;         // of both operands
 constexpr int kRawStages = 6;      // the checkpoint's bytes
 constexpr int kHalf = 128;         // inputs, and outputs, that one CTA loads
 constexpr int kOperandBytes = kHalf * kStepT * 2;            // 16 KB
 constexpr int kGroupBytes = 64 * kStepT * 2;                 // 64 elements of every token
 constexpr int kRawBytes = kHalf * kStepT;                    // 8 KB
+constexpr int kScaleBytes = kStepT * 16;                     // the steps of 4 blocks of every token
 constexpr int kEpilogueWarps = 4;
 constexpr int kTurnPitch = 32 * 2 + 16;                      // bytes of a row of a turned 32 x 32 tile
 constexpr int kTurnBytes = 32 * kTurnPitch;
-constexpr int kYAt = kXStages * kOperandBytes;
-constexpr int kRawAt = kYAt + kYStages * kOperandBytes;
-constexpr int kTurnAt = kRawAt + kRawStages * kRawBytes;
+constexpr int kYAt = kStages * kOperandBytes;
+constexpr int kRawAt = kYAt + kStages * kOperandBytes;
+constexpr int kScaleAt = kRawAt + kRawStages * kRawBytes;
+constexpr int kTurnAt = kScaleAt + kRawStages * kScaleBytes;
 constexpr int kBarrierAt = kTurnAt + kEpilogueWarps * kTurnBytes;
-constexpr int kBarriers = 2 * kXStages + 2 * kYStages + 2 * kRawStages + 4;
-constexpr int kSmemBytes = 1024 + kBarrierAt + kBarriers * 8 + 16;
+constexpr int kBarriers = 2 * kStages + 2 * kRawStages + 4;
+constexpr int kSmemBytes = 1024 + kBarrierAt + kBarriers * 8 + 32;
 static_assert(kSmemBytes <= 227 * 1024, "stages exceed shared memory");
-constexpr int kScalesAhead = 2;    // own steps whose scale bytes a converting warp loads ahead
+constexpr int kScalesAhead = 2;    // own steps whose scale bytes are loaded ahead, in registers
 constexpr int kTmemCols = 512;     // two accumulators of 256 fp32 columns
 
-constexpr int kGroups = 2;         // converting groups
+constexpr int kGroups = 3;         // converting groups
 constexpr int kGroupWarps = 4;
-// warp 0: copies of dy; 1: products; 2..9: conversion; 10..13: epilogue; 14: copies of the checkpoint
-constexpr int kFirstEpilogueWarp = 2 + kGroups * kGroupWarps;
-constexpr int kRawWarp = kFirstEpilogueWarp + kEpilogueWarps;
-constexpr int kThreads = 32 * (kRawWarp + 1);
+constexpr int kTurns = 2;          // pairs of warps for the scale bytes
+
+// Warps by role.  Warp w runs on the SM's scheduler w mod 4.  Scheduler 1 has
+// the thread that issues the products and none of the converting warps: each
+// of its waits goes through the scheduler's queue for shared memory, and took
+// about 250 clocks of a step's 512 behind their loads and stores.
+enum Role { kRoleProducts, kRoleGrads, kRoleRaw, kRoleScales, kRoleConvert, kRoleEpilogue };
+struct Seat {
+    Role role;
+    uint32_t index;   // among the warps of its role
+};
+constexpr int kConvertWarps = kGroups * kGroupWarps;
+static_assert(kConvertWarps == 12 && kTurns == 2, "seats");
+__device__ __forceinline__ Seat seat_of(uint32_t warp)
+{
+    const uint32_t row = warp / 4, col = warp % 4;
+    if (col == 1) {
+        switch (row) {
+        case 0: return {kRoleProducts, 0};
+        case 1: return {kRoleGrads, 0};
+        case 2: return {kRoleRaw, 0};
+        case 3: return {kRoleEpilogue, 1};
+        default: return {kRoleScales, row - 4};
+        }
+    }
+    if (row < 4)
+        return {kRoleConvert, row * 3 + (col ? col - 1 : 0)};
+    if (row == 4)
+        return {kRoleEpilogue, col};
+    return {kRoleScales, col ? 3u : 2u};
+}
+constexpr int kThreads = 32 * 23;
 
 constexpr uint64_t kWaitNs = 4ull * 1000 * 1000 * 1000;
 
@@ -189,29 +218,19 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return done != 0;
-}
-
 // Waits for the phase of parity `parity`; false if that took over kWaitNs or
-// another wait of this CTA has run out (`failed`, shared memory).  The clock
-// is first read after 1,024 tries: reading it before the first retry added
-// about a microsecond to every wait that had to wait at all.
-template <bool CLUSTER = false>
+// another wait of this CTA has run out (`failed`, shared memory).  Waits that
+// poll slow down each other and every arrival, and two dozen warps wait in this
+// kernel: those whose answer is not urgent sleep NS nanoseconds between tries.
+template <int NS>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* failed)
 {
     uint64_t t0 = 0;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
-        if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
+        if (mbar_try_wait(bar, parity))
             return true;
+        if (NS)
+            __nanosleep(NS);
         if ((i & 1023) == 1023) {
             const uint64_t t = global_ns();
             if (!t0)
@@ -223,6 +242,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     *failed = 1;
     return false;
 }
+constexpr int kNow = 0, kSoon = 64, kLater = 500;   // how long a wait sleeps between tries
 
 // A box of a matrix into this CTA's shared memory at dst; its bytes count on
 // this CTA's barrier `bar`.
@@ -322,7 +342,8 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
 }
 
 // The step 2^(s - 127) of a scale byte in both halves of a word, in type DT.
-// binary16 holds it for s in [103, 142]; others take convert4_wide.
+// binary16 holds it for s in [103, 142]; another is kept as the byte itself
+// under a mark (0xFFFF, which no step has), for convert4_wide.
 template <int DT>
 __device__ __forceinline__ uint32_t step2(uint32_t s)
 {
@@ -330,6 +351,8 @@ __device__ __forceinline__ uint32_t step2(uint32_t s)
         const uint32_t h = s == kAct8Bad ? 0x7FC0u : (s ? s << 7 : 0x0040u);
         return h * 0x10001u;
     }
+    if (s < 103 || (s > 142 && s != kAct8Bad))
+        return 0xFFFF0000u | s;
     const uint32_t h = s == kAct8Bad ? 0x7E00u : s >= 113 ? (s - 112) << 10 : 0x0400u >> (113 - s);
     return h * 0x10001u;
 }
@@ -377,53 +400,35 @@ struct WgradArgs {
     Plan plan;
 };
 
-// The scale bytes of 128 inputs from block b on, of token t, as a word (a
-// block or token that does not exist gets the step 1).  Rows need no alignment:
-// away from the ends of the array the word is cut out of the two aligned words
-// around it, which lie in this and the neighbouring rows.
-__device__ __forceinline__ uint32_t load_scales(const WgradArgs& a, uint64_t t, uint32_t b, uint32_t blocks)
+// A word from global memory where `there` says so, else any.  Nothing here or in
+// the caller looks at it before it is needed, so that loads for later steps
+// stay in flight.
+__device__ __forceinline__ uint32_t load_word(const void* p, bool there)
 {
-    if (t >= a.tokens)
-        return 0x7F7F7F7Fu;
-    const uint8_t* p = a.scale + t * a.scale_pitch + b;
-    if (b + 4 <= blocks) {
-        const uint32_t phase = (uint32_t)(uintptr_t)p & 3;
-        if (phase == 0)
-            return __ldg(reinterpret_cast<const uint32_t*>(p));
-        if (a.scale_pitch >= 4 && t > 0 && t + 1 < a.tokens) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p - phase);
-            return __funnelshift_r(__ldg(w), __ldg(w + 1), phase * 8);
-        }
-    }
-    uint32_t w = 0x7F7F7F7Fu;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        if (b + i < blocks)
-            w = (w & ~(0xFFu << (8 * i))) | (uint32_t)p[i] << (8 * i);
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0x7F7F7F7F;\n\t"
+                 "@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "=r"(w)
+                 : "l"(p), "r"((uint32_t)there));
     return w;
 }
 
-// 16 elements of one token.
-struct Chunk {
-    uint4 q;
-    uint32_t s;
-};
-
+// 16 elements of one token and their step: 32 bytes of 16-bit values.
 template <int DT>
-__device__ __forceinline__ void convert_chunk(const Chunk& k, uint4& lo, uint4& hi)
+__device__ __forceinline__ void convert_chunk(uint4 q, uint32_t step, uint4& lo, uint4& hi)
 {
-    if (DT == ZERO_F16 && (k.s < 103 || (k.s > 142 && k.s != kAct8Bad))) {
-        const uint2 x = convert4_wide(k.q.x, k.s), y = convert4_wide(k.q.y, k.s);
-        const uint2 z = convert4_wide(k.q.z, k.s), w = convert4_wide(k.q.w, k.s);
+    if (DT == ZERO_F16 && step >> 16 == 0xFFFFu) {
+        const uint32_t s = step & 0xFF;
+        const uint2 x = convert4_wide(q.x, s), y = convert4_wide(q.y, s);
+        const uint2 z = convert4_wide(q.z, s), w = convert4_wide(q.w, s);
         lo = make_uint4(x.x, x.y, y.x, y.y);
         hi = make_uint4(z.x, z.y, w.x, w.y);
         return;
     }
-    const uint32_t step = step2<DT>(k.s);
-    convert4<DT>(k.q.x, step, lo.x, lo.y);
-    convert4<DT>(k.q.y, step, lo.z, lo.w);
-    convert4<DT>(k.q.z, step, hi.x, hi.y);
-    convert4<DT>(k.q.w, step, hi.z, hi.w);
+    convert4<DT>(q.x, step, lo.x, lo.y);
+    convert4<DT>(q.y, step, lo.z, lo.w);
+    convert4<DT>(q.z, step, hi.x, hi.y);
+    convert4<DT>(q.w, step, hi.z, hi.w);
 }
 
 __device__ __forceinline__ void store_shared16(uint32_t addr, uint4 v)
@@ -448,28 +453,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     pdl_entry();
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t bars = base + kBarrierAt;
-    const uint32_t full_x = bars, empty_x = full_x + 8 * kXStages;
-    const uint32_t full_y = empty_x + 8 * kXStages, empty_y = full_y + 8 * kYStages;
-    const uint32_t raw_full = empty_y + 8 * kYStages, raw_empty = raw_full + 8 * kRawStages;
+    const uint32_t full = bars, empty = full + 8 * kStages;
+    const uint32_t raw_full = empty + 8 * kStages, raw_empty = raw_full + 8 * kRawStages;
     const uint32_t tmem_full = raw_empty + 8 * kRawStages, tmem_empty = tmem_full + 16;
     uint32_t* words = reinterpret_cast<uint32_t*>(raw + (bars + 8 * kBarriers - smem_u32(raw)));
     volatile uint32_t* failed = words + 1;
     const uint32_t rank = cluster_rank();
     const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Seat seat = seat_of(warp);
 
     if (threadIdx.x == 0) {
         *failed = 0;
-        for (int s = 0; s < kXStages; ++s) {
-            mbar_init(full_x + 8 * s, 2 * kGroupWarps);
-            mbar_init(empty_x + 8 * s, 1);
-        }
-        for (int s = 0; s < kYStages; ++s) {
-            mbar_init(full_y + 8 * s, 1);
-            mbar_init(empty_y + 8 * s, 1);
+        for (int g = 0; g < kGroups; ++g)
+            words[2 + g] = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + 8 * s, 2 * kGroupWarps + 1);   // both CTAs' conversions, and dy's bytes
+            mbar_init(empty + 8 * s, 1);
         }
         for (int s = 0; s < kRawStages; ++s) {
-            mbar_init(raw_full + 8 * s, 1);
+            mbar_init(raw_full + 8 * s, 3);
             mbar_init(raw_empty + 8 * s, kGroupWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         total += t.k1 - t.k0;
     }
 
-    if (warp == 0) {
+    if (seat.role == kRoleGrads) {
         if (lane == 0) {   // copies of dy
             uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
             bool ok = true;
@@ -504,19 +507,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Unit t = unit_at(a.plan, u);
                 const int x = (int)(t.to * kTileO + rank * kHalf);
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    if (!wait_phase(empty_y + 8 * stage, phase ^ 1, failed)) {
+                    if (!wait_phase<kSoon>(empty + 8 * stage, phase ^ 1, failed)) {
                         ok = false;
                         break;
                     }
                     if (rank == 0)
-                        mbar_arrive_expect_tx(full_y + 8 * stage, 2 * kOperandBytes);
-                    const uint32_t bar = map_shared(full_y + 8 * stage, 0);
+                        mbar_arrive_expect_tx(full + 8 * stage, 2 * kOperandBytes);
+                    const uint32_t bar = map_shared(full + 8 * stage, 0);
                     const uint32_t dst = base + kYAt + stage * kOperandBytes;
                     tma_box(dst, &dy, x, (int)(k * kStepT), bar);
                     tma_box(dst + kGroupBytes, &dy, x + 64, (int)(k * kStepT), bar);
                     armed |= 1u << stage;
                     armed_phase = (armed_phase & ~(1u << stage)) | phase << stage;
-                    if (++stage == kYStages) {
+                    if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -525,42 +528,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // The pair does not end under its own copies: both CTAs' bytes count on
             // the first one's barriers, and the other waits for it below.
             if (rank == 0)
-                for (uint32_t s = 0; s < kYStages; ++s)
+                for (uint32_t s = 0; s < kStages; ++s)
                     if (armed >> s & 1)
-                        mbar_wait(full_y + 8 * s, armed_phase >> s & 1, kWaitNs);
+                        mbar_wait(full + 8 * s, armed_phase >> s & 1, kWaitNs);
         }
-    } else if (warp == 1) {
+    } else if (seat.role == kRoleProducts) {
         if (lane == 0 && rank == 0) {   // products
-            uint32_t xs = 0, x_phase = 0, ys = 0, y_phase = 0, buf = 0, buf_phase = 0;
+            uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (uint32_t u = pair; u < a.plan.units && ok; u += pairs) {
                 const Unit t = unit_at(a.plan, u);
-                ok = wait_phase<true>(tmem_empty + 8 * buf, buf_phase ^ 1, failed);
+                ok = wait_phase<kNow>(tmem_empty + 8 * buf, buf_phase ^ 1, failed);
                 if (!ok)
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tmem + buf * kTileO;
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    ok = wait_phase(full_y + 8 * ys, y_phase, failed) &&
-                         wait_phase<true>(full_x + 8 * xs, x_phase, failed);
+                    ok = wait_phase<kNow>(full + 8 * stage, phase, failed);
                     if (!ok)
                         break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint64_t xd = operand_desc(base + xs * kOperandBytes);
-                    const uint64_t yd = operand_desc(base + kYAt + ys * kOperandBytes);
+                    const uint64_t xd = operand_desc(base + stage * kOperandBytes);
+                    const uint64_t yd = operand_desc(base + kYAt + stage * kOperandBytes);
 #pragma unroll
                     for (int j = 0; j < kStepT / 16; ++j)   // 16 tokens: 2048 bytes further
                         mma_pair(acc, xd + j * (2048 >> 4), yd + j * (2048 >> 4), instr_desc<DT>(),
                                  k > t.k0 || j > 0);
-                    commit_pair(empty_x + 8 * xs);
-                    commit_pair(empty_y + 8 * ys);
-                    if (++xs == kXStages) {
-                        xs = 0;
-                        x_phase ^= 1;
-                    }
-                    if (++ys == kYStages) {
-                        ys = 0;
-                        y_phase ^= 1;
+                    commit_pair(empty + 8 * stage);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
                     }
                 }
                 if (!ok)
@@ -570,92 +567,64 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 buf_phase ^= buf == 0;
             }
         }
-    } else if (warp < kFirstEpilogueWarp) {
+    } else if (seat.role == kRoleConvert) {
         // conversion: group g takes steps g, g + 2, ...  A thread takes 16 inputs of
         // either half at tokens tok and tok + 32.  Lanes 0..3 and 4..7 of a quarter
         // warp take tokens that differ in bits 0 and 2, whose swizzles keep its
         // 16-byte loads, and its stores, on different banks.
-        const uint32_t group = (warp - 2) / kGroupWarps;
+        const uint32_t group = seat.index / kGroupWarps;
+        const bool leads = seat.index % kGroupWarps == 0;
+        volatile uint32_t* stopped = words + 2 + group;   // set by the leading warp before the barrier
         const uint32_t p = lane / 4, j = lane % 4;
-        const uint32_t tok = (warp - 2) % kGroupWarps * 8 + (p / 2 ^ (p & 1) * 5);
+        const uint32_t tok = seat.index % kGroupWarps * 8 + (p / 2 ^ (p & 1) * 5);
         const uint32_t sw = tok & 7;
         const uint32_t from0 = tok * 128 + (j ^ sw) * 16, from1 = tok * 128 + (4 + j ^ sw) * 16;
         const uint32_t to0 = tok * 128 + (2 * j ^ sw) * 16, to1 = tok * 128 + (2 * j + 1 ^ sw) * 16;
-        // the step that this thread's next scale bytes belong to
-        const uint32_t blocks = (uint32_t)((a.ins + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK);
-        uint32_t at_u = pair, at_k = 0, at_k1 = 0, at_b = 0, skip = group;
-        uint32_t sc[kScalesAhead][2];
-        auto fetch = [&](uint32_t (&w)[2]) {
-            at_k += skip;
-            while (at_k >= at_k1) {
-                const Unit t = unit_at(a.plan, at_u);
-                at_k = t.k0 + (at_k - at_k1);
-                at_k1 = t.k1;
-                at_b = (t.ti * kTileI + rank * kHalf) / ZERO_ACT8_BLOCK;
-                at_u += pairs;
-            }
-            const uint64_t t = (uint64_t)at_k * kStepT + tok;
-            w[0] = load_scales(a, t, at_b, blocks);
-            w[1] = load_scales(a, t + 32, at_b, blocks);
-            skip = kGroups;
-        };
-#pragma unroll
-        for (int i = 0; i < kScalesAhead; ++i)
-            if (group + i * kGroups < total)
-                fetch(sc[i]);
         uint32_t stage = group, phase = 0, rstage = group, rphase = 0;
-        static_assert(kGroups <= kXStages && kGroups <= kRawStages, "a group's first stage");
-        bool ok = true;   // the same in the whole warp
-        for (uint32_t n0 = group; n0 < total && ok; n0 += kGroups * kScalesAhead)
-#pragma unroll
-            for (int h = 0; h < kScalesAhead; ++h) {
-                const uint32_t n = n0 + h * kGroups;
-                if (n >= total || !ok)
-                    break;
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(raw_full + 8 * rstage, rphase, failed));
-                if (!ok)
-                    break;
-                const uint32_t src = base + kRawAt + rstage * kRawBytes;
-                Chunk k[4];
-                k[0].q = load_shared16(src + from0);
-                k[1].q = load_shared16(src + from1);
-                k[2].q = load_shared16(src + 32 * 128 + from0);
-                k[3].q = load_shared16(src + 32 * 128 + from1);
-                k[0].s = sc[h][0] >> (j / 2 * 8) & 0xFF;
-                k[1].s = sc[h][0] >> (16 + j / 2 * 8) & 0xFF;
-                k[2].s = sc[h][1] >> (j / 2 * 8) & 0xFF;
-                k[3].s = sc[h][1] >> (16 + j / 2 * 8) & 0xFF;
-                uint4 v[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    convert_chunk<DT>(k[i], v[2 * i], v[2 * i + 1]);
-                if (n + kGroups * kScalesAhead < total)
-                    fetch(sc[h]);
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(empty_x + 8 * stage, phase ^ 1, failed));
-                if (!ok)
-                    break;
-                const uint32_t dst = base + stage * kOperandBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {   // half i % 2, tokens + 32 (i / 2)
-                    store_shared16(dst + i % 2 * kGroupBytes + i / 2 * 32 * 128 + to0, v[2 * i]);
-                    store_shared16(dst + i % 2 * kGroupBytes + i / 2 * 32 * 128 + to1, v[2 * i + 1]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive_cluster(map_shared(full_x + 8 * stage, 0));
-                    mbar_arrive(raw_empty + 8 * rstage);
-                }
-                if ((stage += kGroups) >= kXStages) {
-                    stage -= kXStages;
-                    phase ^= 1;
-                }
-                if ((rstage += kGroups) >= kRawStages) {
-                    rstage -= kRawStages;
-                    rphase ^= 1;
-                }
+        static_assert(kGroups <= kStages && kGroups <= kRawStages, "a group's first stage");
+        for (uint32_t n = group; n < total; n += kGroups) {
+            // one warp of the group waits, the others for it
+            if (leads && !(wait_phase<kNow>(raw_full + 8 * rstage, rphase, failed) &&
+                           wait_phase<kNow>(empty + 8 * stage, phase ^ 1, failed)))
+                *stopped = 1;
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * kGroupWarps) : "memory");
+            if (*stopped)
+                break;
+            const uint32_t src = base + kRawAt + rstage * kRawBytes;
+            const uint32_t sc = base + kScaleAt + rstage * kScaleBytes + tok * 16 + j / 2 * 8;
+            const uint32_t dst = base + stage * kOperandBytes;
+            // Rolled: the loop body then stays in the warp scheduler's instruction
+            // cache, which twenty warps in five roles otherwise thrash.
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {   // tokens tok, tok + 32
+                uint32_t s0, s1;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(sc + h * 32 * 16));
+                const uint4 q0 = load_shared16(src + h * 32 * 128 + from0);
+                const uint4 q1 = load_shared16(src + h * 32 * 128 + from1);
+                uint4 lo, hi;
+                convert_chunk<DT>(q0, s0, lo, hi);
+                store_shared16(dst + h * 32 * 128 + to0, lo);
+                store_shared16(dst + h * 32 * 128 + to1, hi);
+                convert_chunk<DT>(q1, s1, lo, hi);
+                store_shared16(dst + kGroupBytes + h * 32 * 128 + to0, lo);
+                store_shared16(dst + kGroupBytes + h * 32 * 128 + to1, hi);
             }
-    } else if (warp == kRawWarp) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                arrive_cluster(map_shared(full + 8 * stage, 0));
+                mbar_arrive(raw_empty + 8 * rstage);
+            }
+            if ((stage += kGroups) >= kStages) {
+                stage -= kStages;
+                phase ^= 1;
+            }
+            if ((rstage += kGroups) >= kRawStages) {
+                rstage -= kRawStages;
+                rphase ^= 1;
+            }
+        }
+    } else if (seat.role == kRoleRaw) {
         if (lane == 0) {   // copies of the checkpoint
             uint32_t stage = 0, phase = 0, armed = 0, armed_phase = 0;
             bool ok = true;
@@ -663,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Unit t = unit_at(a.plan, u);
                 const int x = (int)(t.ti * kTileI + rank * kHalf);
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    ok = wait_phase(raw_empty + 8 * stage, phase ^ 1, failed);
+                    ok = wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed);
                     if (!ok)
                         break;
                     mbar_arrive_expect_tx(raw_full + 8 * stage, kRawBytes);
@@ -681,6 +650,84 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (armed >> s & 1)
                     mbar_wait(raw_full + 8 * s, armed_phase >> s & 1, kWaitNs);
         }
+    } else if (seat.role == kRoleScales) {
+        // scale bytes: pair g of the warps takes steps g, g + kTurns, ...; lane l of
+        // its warp w loads those of token 32 w + l and leaves their steps, in the
+        // order of blocks 0, 2, 1, 3 (a converting thread takes two 64 inputs apart),
+        // beside the bytes.  Rows of scale bytes need no alignment: a word is cut out
+        // of the two aligned words around it.  Those lie in this row and its
+        // neighbours, except at the array's first and last row, which are read by
+        // bytes.  A lane's phase is the same in all its rows (a multiple of 64 tokens
+        // apart).  Blocks that do not exist get any step: their inputs are zero and
+        // their sums are not stored.
+        const uint32_t half = seat.index % 2, turn = seat.index / 2;
+        const uint32_t blocks = (uint32_t)((a.ins + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK);
+        const uint32_t shift =
+            (uint32_t)((uintptr_t)(a.scale + (half * 32 + lane) * a.scale_pitch) & 3) * 8;
+        const uint64_t hop = (uint64_t)kTurns * kStepT * a.scale_pitch;
+        uint32_t u = pair, k = 0, k1 = 0, skip = turn;   // the step of the next scale bytes
+        uint32_t exist = 0;
+        const uint8_t* p = nullptr;
+        uint32_t w0[kScalesAhead], w1[kScalesAhead];
+        auto fetch = [&](uint32_t& lo, uint32_t& hi) {
+            k += skip;
+            p += hop;
+            skip = kTurns;
+            if (k >= k1) {
+                do {
+                    const Unit r = unit_at(a.plan, u);
+                    u += pairs;
+                    k = r.k0 + (k - k1);
+                    k1 = r.k1;
+                    const uint32_t b = (r.ti * kTileI + rank * kHalf) / ZERO_ACT8_BLOCK;
+                    exist = b < blocks ? min(4u, blocks - b) : 0;
+                    p = a.scale + ((uint64_t)k * kStepT + half * 32 + lane) * a.scale_pitch + b;
+                } while (k >= k1);
+            }
+            const uint64_t t0 = (uint64_t)k * kStepT;   // the step's first token
+            if (t0 > 0 && t0 + kStepT < a.tokens && a.scale_pitch >= 8) {
+                lo = load_word(p - shift / 8, exist);
+                hi = load_word(p - shift / 8 + 4, exist && shift);
+                return;
+            }
+            const uint64_t t = t0 + half * 32 + lane;
+            uint32_t w = 0x7F7F7F7Fu;
+            if (t < a.tokens)
+                for (uint32_t i = 0; i < exist; ++i)
+                    w = (w & ~(0xFFu << (8 * i))) | (uint32_t)p[i] << (8 * i);
+            lo = w << shift;
+            hi = __funnelshift_l(w, 0, shift);
+        };
+#pragma unroll
+        for (int i = 0; i < kScalesAhead; ++i)
+            if (turn + i * kTurns < total)
+                fetch(w0[i], w1[i]);
+        uint32_t stage = turn, phase = 0;
+        static_assert(kTurns <= kRawStages, "a pair's first stage");
+        bool ok = true;
+        for (uint32_t n0 = turn; n0 < total && ok; n0 += kTurns * kScalesAhead)
+#pragma unroll
+            for (int i = 0; i < kScalesAhead; ++i) {
+                const uint32_t n = n0 + i * kTurns;
+                if (n >= total || !ok)
+                    break;
+                ok = __all_sync(0xFFFFFFFFu, wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed));
+                if (!ok)
+                    break;
+                const uint32_t w = __funnelshift_r(w0[i], w1[i], shift);
+                store_shared16(base + kScaleAt + stage * kScaleBytes + (half * 32 + lane) * 16,
+                               make_uint4(step2<DT>(w & 0xFF), step2<DT>(w >> 16 & 0xFF),
+                                          step2<DT>(w >> 8 & 0xFF), step2<DT>(w >> 24)));
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(raw_full + 8 * stage);
+                if (n + kTurns * kScalesAhead < total)
+                    fetch(w0[i], w1[i]);
+                if ((stage += kTurns) >= kRawStages) {
+                    stage -= kRawStages;
+                    phase ^= 1;
+                }
+            }
     } else {
         // epilogue: warp w of the CTA may read the tensor memory lanes 32 (w mod 4) .. + 31;
         // a lane is an input, a column an output
@@ -692,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t buf = 0, buf_phase = 0;
         for (uint32_t u = pair; u < a.plan.units; u += pairs) {
             const Unit t = unit_at(a.plan, u);
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_phase(tmem_full + 8 * buf, buf_phase, failed));
+            const bool ok = __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t r = rank * kHalf + quarter * 32 + lane;
             const uint64_t i = (uint64_t)t.ti * kTileI + r;
@@ -744,14 +791,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 } else if (i < a.ins) {
                     uint16_t* p = a.dw + (o0 + c) * a.dw_pitch + i;
                     const uint32_t n = o0 + c < a.outs ? (uint32_t)min((uint64_t)32, a.outs - o0 - c) : 0;
-                    float old[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        old[j] = a.add && j < n ? widen1<DT>(p[j * a.dw_pitch]) : 0.0f;
+                    for (int h = 0; h < 32; h += 8) {
+                        float old[8];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n)
-                            p[j * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[j]) * gain + old[j]);
+                        for (int j = 0; j < 8; ++j)
+                            old[j] = a.add && h + j < n ? widen1<DT>(p[(h + j) * a.dw_pitch]) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (h + j < n)
+                                p[(h + j) * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[h + j]) * gain + old[j]);
+                    }
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
