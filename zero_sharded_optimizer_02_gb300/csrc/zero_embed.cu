@@ -2,12 +2,13 @@
 //
 // The gradient's row v is the sum of d_out over the tokens numbered v.  The
 // tokens are sorted by number, stably (so equal numbers stay in token order),
-// and every row of the table is then one contiguous run of the sorted order,
-// summed by one CTA's threads with no atomics.  Numbers are far from evenly
-// spread: a frequent token takes thousands of rows.  A run is therefore cut
-// at the multiples of kRun positions: pieces that fill a whole such cell are
-// summed first, each on its own, into fp32 partial rows, and a second launch
-// adds the partial rows of a long run, and its two ends, in their order.
+// and every row of the table is then one contiguous run of the sorted order.
+// Numbers are far from evenly spread: a frequent token takes thousands of rows
+// of d_out, so the work is split evenly over the sorted positions, not over the
+// table's rows: a thread sums 8 columns of a cell of 32 positions, run by run.
+// A run inside one cell is stored at once; one that crosses cells leaves an
+// fp32 partial row in each, and a second launch adds those up in their order.
+// No atomics: the result does not depend on scheduling.
 #include "zero_train_device.cuh"
 
 namespace zero {
@@ -20,6 +21,23 @@ __device__ __forceinline__ int64_t load_id(const void* ids, uint32_t bytes, uint
 {
     return bytes == 8 ? static_cast<const int64_t*>(ids)[i]
                       : (int64_t) static_cast<const int32_t*>(ids)[i];
+}
+
+// N token numbers from i on, `stride` apart (-1 past n); the loads are issued
+// together, which a branch on their size in between would prevent.
+template <int N>
+__device__ __forceinline__ void load_ids(const void* ids, uint32_t bytes, uint32_t i, uint32_t stride, uint32_t n,
+                                         int64_t (&id)[N])
+{
+    if (bytes == 8) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            id[k] = i + k * stride < n ? static_cast<const int64_t*>(ids)[i + k * stride] : -1;
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            id[k] = i + k * stride < n ? static_cast<const int32_t*>(ids)[i + k * stride] : -1;
+    }
 }
 
 // -- lookup ---------------------------------------------------------------------------
@@ -75,6 +93,20 @@ __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupArgs a)
 
 // -- sort -----------------------------------------------------------------------------
 
+// The lanes whose digit d (of at most BITS bits) equals this lane's, among those
+// with `in`.  One ballot a bit: __match_any_sync took ten times as long.
+template <int BITS>
+__device__ __forceinline__ uint32_t peers_of(uint32_t d, bool in)
+{
+    uint32_t peers = __ballot_sync(0xFFFFFFFFu, in);
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+        const uint32_t bit = d >> b & 1;
+        peers &= __ballot_sync(0xFFFFFFFFu, bit) ^ (bit - 1);
+    }
+    return peers;
+}
+
 // One stable pass of a least-significant-digit radix sort of (number, token)
 // pairs is three launches: digit counts of every tile, their exclusive sums
 // over (digit, tile), and the move.  Numbers outside the table sort as
@@ -87,21 +119,19 @@ constexpr int kPerWarp = kTile / kWarps;    // consecutive tokens of one warp
 
 struct SortArgs {
     const void* ids;        // first pass: the caller's numbers
-    const uint32_t* keys;   // later passes
-    const uint32_t* toks;
-    uint32_t* keys_out;
-    uint32_t* toks_out;
+    const uint2* in;        // later passes: (number, token) pairs
+    uint2* out;
     uint32_t* counts;       // [digit][tile]
     uint32_t* bad;
     uint32_t n, ntiles, shift, id_bytes, vocab;
 };
 
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i)
+__device__ __forceinline__ uint2 sort_pair(const SortArgs& a, uint32_t i)
 {
     if (!a.ids)
-        return a.keys[i];
+        return a.in[i];
     const int64_t id = load_id(a.ids, a.id_bytes, i);
-    return id >= 0 && id < (int64_t)a.vocab ? (uint32_t)id : a.vocab;
+    return make_uint2(id >= 0 && id < (int64_t)a.vocab ? (uint32_t)id : a.vocab, i);
 }
 
 __global__ void __launch_bounds__(kThreads) k_sort_count(const SortArgs a)
@@ -114,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_sort_count(const SortArgs a)
     for (int j = threadIdx.x; j < kTile; j += kThreads) {
         const uint32_t i = blockIdx.x * kTile + j;
         if (i < a.n) {
-            atomicAdd(&h[(sort_key(a, i) >> a.shift) & (kDigits - 1)], 1u);
+            atomicAdd(&h[(sort_pair(a, i).x >> a.shift) & (kDigits - 1)], 1u);
             if (a.ids && a.bad && load_id(a.ids, a.id_bytes, i) >= (int64_t)a.vocab)
                 atomicOr(a.bad, 1u);
         }
@@ -124,18 +154,26 @@ __global__ void __launch_bounds__(kThreads) k_sort_count(const SortArgs a)
         a.counts[(uint64_t)d * a.ntiles + blockIdx.x] = h[d];
 }
 
-// Exclusive sums of `n` counts in place, by one CTA.
+// Exclusive sums of `n` counts in place, by one CTA, kScanItems a thread at a
+// time (the array has room for a multiple of kScanItems).
 constexpr int kScanThreads = 1024;
+constexpr int kScanItems = 16;
 __global__ void __launch_bounds__(kScanThreads) k_sort_scan(uint32_t* counts, uint32_t n)
 {
     __shared__ uint32_t warp_sums[32];
     pdl_entry();
     uint32_t carry = 0;
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    for (uint32_t i0 = 0; i0 < n; i0 += kScanThreads) {
-        const uint32_t i = i0 + threadIdx.x;
-        const uint32_t v = i < n ? counts[i] : 0;
-        uint32_t s = v;
+    for (uint32_t i0 = 0; i0 < n; i0 += kScanThreads * kScanItems) {
+        const uint32_t i = i0 + threadIdx.x * kScanItems;
+        uint4 v[kScanItems / 4];
+        uint32_t s = 0;
+#pragma unroll
+        for (int k = 0; k < kScanItems / 4; ++k) {
+            v[k] = i + 4 * k < n ? reinterpret_cast<const uint4*>(counts + i)[k] : make_uint4(0, 0, 0, 0);
+            s += v[k].x + v[k].y + v[k].z + v[k].w;
+        }
+        const uint32_t own = s;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
@@ -152,11 +190,17 @@ __global__ void __launch_bounds__(kScanThreads) k_sort_scan(uint32_t* counts, ui
             if (lane >= (uint32_t)d)
                 w += o;
         }
-        const uint32_t before = warp ? __shfl_sync(0xFFFFFFFFu, w, warp - 1) : 0;
-        const uint32_t total = __shfl_sync(0xFFFFFFFFu, w, 31);
-        if (i < n)
-            counts[i] = carry + before + s - v;
-        carry += total;
+        const uint32_t ahead = __shfl_sync(0xFFFFFFFFu, w, warp ? warp - 1 : 0);
+        uint32_t at = carry + (warp ? ahead : 0) + s - own;
+        carry += __shfl_sync(0xFFFFFFFFu, w, 31);
+#pragma unroll
+        for (int k = 0; k < kScanItems / 4; ++k) {
+            const uint4 c = v[k];
+            v[k] = make_uint4(at, at + c.x, at + c.x + c.y, at + c.x + c.y + c.z);
+            at += c.x + c.y + c.z + c.w;
+            if (i + 4 * k < n)
+                reinterpret_cast<uint4*>(counts + i)[k] = v[k];
+        }
         __syncthreads();
     }
 }
@@ -170,18 +214,19 @@ __global__ void __launch_bounds__(kThreads) k_sort_move(const SortArgs a)
         h[warp][d] = 0;
     __syncwarp();
     constexpr int kRounds = kPerWarp / 32;
-    uint32_t key[kRounds], rank[kRounds];
+    uint2 pair[kRounds];
+    uint32_t rank[kRounds];
     const uint32_t i0 = blockIdx.x * kTile + warp * kPerWarp + lane;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const uint32_t i = i0 + r * 32;
-        key[r] = i < a.n ? sort_key(a, i) : 0;
+        pair[r] = i < a.n ? sort_pair(a, i) : make_uint2(0, 0);
     }
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const bool in = i0 + r * 32 < a.n;
-        const uint32_t d = in ? (key[r] >> a.shift) & (kDigits - 1) : kDigits;
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+        const uint32_t d = (pair[r].x >> a.shift) & (kDigits - 1);
+        const uint32_t peers = peers_of<kDigitBits>(d, in);
         const uint32_t before = __popc(peers & ((1u << lane) - 1));
         uint32_t base = 0;
         if (in)
@@ -207,42 +252,304 @@ __global__ void __launch_bounds__(kThreads) k_sort_move(const SortArgs a)
     for (int r = 0; r < kRounds; ++r) {
         const uint32_t i = i0 + r * 32;
         if (i < a.n) {
-            const uint32_t at = h[warp][(key[r] >> a.shift) & (kDigits - 1)] + rank[r];
-            a.keys_out[at] = key[r];
-            a.toks_out[at] = a.ids ? i : a.toks[i];
+            a.out[h[warp][(pair[r].x >> a.shift) & (kDigits - 1)] + rank[r]] = pair[r];
         }
     }
 }
 
+// Up to kClusterTokens tokens are sorted in one launch, by a cluster of up to 8
+// CTAs that keep the pairs in shared memory: CTA r holds positions [r * per, (r + 1)
+// * per) of the order so far, a thread I of them.  A pass counts each warp's
+// digits, adds the counts up over warps and, through the other CTAs' shared
+// memory, over CTAs, and moves every pair to its new place: into the CTA that
+// holds it, or in the last pass to global memory.  The multi-launch passes
+// take about 5 us each for their launches alone.
+constexpr int kClusterCtas = 8;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterItems = 8;
+constexpr uint32_t kClusterTokens = kClusterCtas * kClusterThreads * kClusterItems;
+constexpr int kClusterDigitBits = 9;
+constexpr int kClusterDigits = 1 << kClusterDigitBits;
+
+struct ClusterSort {
+    const void* ids;
+    uint2* out;
+    uint32_t* bad;
+    uint32_t n, id_bytes, vocab, bits, passes;   // bits of a digit
+};
+
+constexpr size_t cluster_sort_smem(int items)
+{
+    return (size_t)kClusterThreads * items * sizeof(uint2) + kClusterWarps * kClusterDigits * sizeof(uint16_t) +
+           (2 * kClusterDigits + 32) * sizeof(uint32_t);
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int I>
+__global__ void __launch_bounds__(kClusterThreads) k_sort_cluster(const ClusterSort a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr uint32_t per = kClusterThreads * I;
+    uint2* pairs = reinterpret_cast<uint2*>(smem);
+    uint16_t* counts = reinterpret_cast<uint16_t*>(smem + per * sizeof(uint2));   // [warp][digit]
+    uint32_t* total = reinterpret_cast<uint32_t*>(counts + kClusterWarps * kClusterDigits);
+    uint32_t* first = total + kClusterDigits;   // where the CTA's pairs of a digit go
+    uint32_t* warp_sums = first + kClusterDigits;
+    pdl_entry();
+    uint32_t rank_in_cluster, ctas;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_in_cluster));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t at0 = warp * 32 * I + lane;        // this thread's places: at0 + 32 i
+    uint2 pair[I];
+    bool bad = false;
+    int64_t id[I];
+    load_ids<I>(a.ids, a.id_bytes, rank_in_cluster * per + at0, 32, a.n, id);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        const uint32_t t = rank_in_cluster * per + at0 + 32 * i;
+        const uint32_t key = id[i] >= 0 && id[i] < (int64_t)a.vocab ? (uint32_t)id[i] : a.vocab;
+        pair[i] = make_uint2(t < a.n ? key : 0xFFFFFFFFu, t);
+        bad |= id[i] >= (int64_t)a.vocab;
+    }
+    if (bad && a.bad)
+        atomicOr(a.bad, 1u);
+    const uint32_t digits = 1u << a.bits, mask = digits - 1;
+    for (uint32_t pass = 0; pass < a.passes; ++pass) {
+        const uint32_t shift = pass * a.bits;
+        for (uint32_t d = threadIdx.x; d < kClusterWarps * digits / 2; d += kClusterThreads)
+            reinterpret_cast<uint32_t*>(counts)[d] = 0;
+        __syncthreads();
+        uint16_t* mine = counts + warp * digits;
+        uint32_t rank[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i)   // places past the end have key 0xFFFFFFFF and no count
+            rank[i] = peers_of<kClusterDigitBits>(pair[i].x >> shift & mask, pair[i].x != 0xFFFFFFFFu);
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const bool in = pair[i].x != 0xFFFFFFFFu;
+            const uint32_t d = pair[i].x >> shift & mask;
+            const uint32_t peers = rank[i];
+            const uint32_t before = __popc(peers & ((1u << lane) - 1));
+            uint32_t base = 0;
+            if (in)
+                base = mine[d];
+            __syncwarp();
+            if (in && before == 0)
+                mine[d] = (uint16_t)(base + __popc(peers));
+            __syncwarp();
+            rank[i] = base + before;
+        }
+        __syncthreads();
+        if (threadIdx.x < digits) {   // over the warps
+            uint32_t sum = 0;
+#pragma unroll
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t c = counts[w * digits + threadIdx.x];
+                counts[w * digits + threadIdx.x] = (uint16_t)sum;
+                sum += c;
+            }
+            total[threadIdx.x] = sum;
+        }
+        cluster_barrier();
+        // over the CTAs, then over the digits
+        uint32_t lower = 0, all = 0;
+        if (threadIdx.x < digits) {
+            const uint32_t word = smem_u32(total + threadIdx.x);
+#pragma unroll
+            for (uint32_t r = 0; r < kClusterCtas; ++r) {
+                if (r < ctas) {
+                    uint32_t addr, v;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(word), "r"(r));
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+                    all += v;
+                    lower += r < rank_in_cluster ? v : 0;
+                }
+            }
+        }
+        uint32_t sum = all;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= (uint32_t)o)
+                sum += v;
+        }
+        if (lane == 31)
+            warp_sums[warp] = sum;
+        __syncthreads();
+        uint32_t w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= (uint32_t)o)
+                w += v;
+        }
+        const uint32_t ahead = __shfl_sync(0xFFFFFFFFu, w, warp ? warp - 1 : 0);
+        if (threadIdx.x < digits)
+            first[threadIdx.x] = (warp ? ahead : 0) + sum - all + lower;
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            if (pair[i].x == 0xFFFFFFFFu)
+                continue;
+            const uint32_t d = pair[i].x >> shift & mask;
+            const uint32_t to = first[d] + mine[d] + rank[i];
+            if (last) {
+                a.out[to] = pair[i];
+            } else {
+                uint32_t addr;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(addr)
+                             : "r"(smem_u32(pairs + to % per)), "r"(to / per));
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(pair[i].x), "r"(pair[i].y)
+                             : "memory");
+            }
+        }
+        // the pairs are in place, and every CTA has read the others' totals
+        cluster_barrier();
+        if (!last)
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                pair[i] = rank_in_cluster * per + at0 + 32 * i < a.n ? pairs[at0 + 32 * i]
+                                                                     : make_uint2(0xFFFFFFFFu, 0);
+    }
+}
+
+template <int I>
+cudaError_t launch_cluster_sort(const ClusterSort& a, void* stream)
+{
+    static std::atomic<uint64_t> allowed{0};
+    allow_smem(k_sort_cluster<I>, cluster_sort_smem(I), allowed);
+    uint32_t ctas = 1;   // a power of two, as clusters are
+    while (ctas < kClusterCtas && ctas * kClusterThreads * I < a.n)
+        ctas *= 2;
+    return launch_train(k_sort_cluster<I>, dim3(ctas), kClusterThreads, cluster_sort_smem(I), ctas, stream, a);
+}
+
+// -- rows of absent tokens ------------------------------------------------------------
+
+// Writes zeros to the rows of absent tokens (of a stored gradient) while
+// k_sort_cluster, launched before it, runs on its 8 SMs: it starts with it and
+// ends after it (pdl_end), so the sums that follow find both done.  It starts
+// only when every CTA of the sort has passed the wait for the work before the
+// call, and reads and writes nothing that the sort writes.
+//
+// CTA `me` takes every kZeroCtas-th group of 32 rows, since the rows of absent
+// tokens crowd at one end of a vocabulary sorted by frequency and one SM writes
+// only about 25 bytes a clock.  It marks its tokens by reading all numbers.
+// Rows of whole 16-byte vectors are bulk copies of kZeroBytes zeroed bytes of
+// shared memory, a thread a row; others are stored by a warp each.  All SMs
+// write at most 4.0 TB/s (a memset of 1 GB), 0.6 of what a copy moves.
+constexpr uint32_t kZeroCtas = 128;
+constexpr int kZeroThreads = 1024;
+constexpr uint32_t kZeroBytes = 8192;
+constexpr uint32_t kMarkWords = 8192;   // groups that a CTA marks at a time
+static_assert((kZeroCtas & (kZeroCtas - 1)) == 0, "a mask finds a group's CTA");
+
+struct ZeroArgs {
+    const void* ids;
+    uint16_t* d_table;
+    uint64_t table_pitch, dim;
+    uint32_t n, id_bytes, vocab, slots;
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
+{
+    __shared__ __align__(16) uint32_t zeros[kZeroBytes / 4];
+    __shared__ uint32_t marks[kMarkWords];
+    pdl_begin(1);
+    const uint32_t me = blockIdx.x;
+    const bool bulk = VEC && a.dim % 8 == 0;
+    if (bulk) {
+        for (uint32_t i = threadIdx.x; i < kZeroBytes / 4; i += kZeroThreads)
+            zeros[i] = 0;
+        fence_proxy_async_smem();
+    }
+    const uint32_t groups = (a.vocab + 31) / 32;
+    const uint32_t mine = me < groups ? (groups - 1 - me) / kZeroCtas + 1 : 0;   // groups of this CTA
+    for (uint32_t lo = 0; lo < mine; lo += kMarkWords) {
+        const uint32_t n = min(mine - lo, kMarkWords);
+        for (uint32_t i = threadIdx.x; i < n; i += kZeroThreads)
+            marks[i] = 0;
+        __syncthreads();
+        constexpr int kBatch = 4;
+        for (uint32_t t = threadIdx.x; t < a.n; t += kZeroThreads * kBatch) {
+            int64_t id[kBatch];
+            load_ids<kBatch>(a.ids, a.id_bytes, t, kZeroThreads, a.n, id);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t v = (uint32_t)id[k], word = v / 32 / kZeroCtas - lo;
+                if (v / 32 % kZeroCtas == me && id[k] >= 0 && id[k] < (int64_t)a.vocab && word < n)
+                    atomicOr(&marks[word], 1u << (v & 31));
+            }
+        }
+        __syncthreads();
+        // row 32 ((lo + i) kZeroCtas + me) + bit for word i of the marks
+        if (bulk) {
+            for (uint32_t r = threadIdx.x; r < n * 32; r += kZeroThreads) {
+                const uint32_t v = ((lo + r / 32) * kZeroCtas + me) * 32 + r % 32;
+                if (v < a.vocab && !(marks[r / 32] >> (r % 32) & 1)) {
+                    char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)v * a.table_pitch);
+                    for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
+                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
+                                     "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
+                                     : "memory");
+                }
+            }
+        } else {
+            for (uint32_t r = threadIdx.x / 32; r < n * 32; r += kZeroThreads / 32) {
+                const uint32_t v = ((lo + r / 32) * kZeroCtas + me) * 32 + r % 32;
+                if (v < a.vocab && !(marks[r / 32] >> (r % 32) & 1))
+                    for (uint32_t s = threadIdx.x % 32; s < a.slots; s += 32)
+                        store8_row<VEC>(a.d_table + (uint64_t)v * a.table_pitch, (uint64_t)s * 8, a.dim,
+                                        make_uint4(0, 0, 0, 0));
+            }
+        }
+        __syncthreads();
+    }
+    if (bulk) {   // the copies read shared memory: not to be left in flight
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    pdl_end(1);
+}
+
 // -- sums -----------------------------------------------------------------------------
 
-constexpr int kRun = 32;        // positions of a cell
-constexpr int kRowsPerCta = 32; // table rows of one CTA
-constexpr int kJoinSlices = kThreads / 32;
+constexpr int kCell = 32;        // positions of a cell
+constexpr int kMaxCells = 32;    // cells of one CTA
+constexpr int kZeroRows = 128;   // table rows of one CTA that looks for absent tokens
+static_assert(kMaxCells * kCell * sizeof(uint2) >= kZeroBytes, "zeros fit where the pairs are");
+constexpr int kJoinCells = kThreads / 32;
 
 struct GradArgs {
     const uint16_t* d_out;
-    const uint32_t* keys;   // sorted
-    const uint32_t* toks;
-    float* parts;           // [cell][slots * 8]
+    const uint2* pairs;     // (number, token), sorted
+    float* parts;           // [cell][2][slots * 8]
     uint16_t* d_table;
     uint64_t d_out_pitch, table_pitch, dim;
     uint32_t n, vocab, slots, cells;
-    uint32_t row_ctas;      // the CTAs before these take cells
-    uint32_t add;
+    uint32_t per_cta;       // cells of one CTA
+    uint32_t cell_ctas;     // CTAs that take cells; the launch's others take table rows
     float scale;
 };
 
 // The first position in [0, n) whose key is >= key (n if none), by one warp:
 // 32 probes a step.
-__device__ uint32_t lower_bound_warp(const uint32_t* keys, uint32_t n, uint32_t key)
+__device__ uint32_t lower_bound_warp(const uint2* pairs, uint32_t n, uint32_t key)
 {
     const uint32_t lane = threadIdx.x % 32;
     uint32_t lo = 0, hi = n;   // the answer is in [lo, hi]
     while (lo < hi) {
         const uint32_t step = (hi - lo + 31) / 32;
         const uint64_t p = (uint64_t)lo + (uint64_t)lane * step;
-        const bool less = p < hi && keys[p] < key;
+        const bool less = p < hi && pairs[p].x < key;
         const uint32_t count = __popc(__ballot_sync(0xFFFFFFFFu, less));   // a prefix of the lanes
         if (count == 0)
             return lo;
@@ -253,157 +560,252 @@ __device__ uint32_t lower_bound_warp(const uint32_t* keys, uint32_t n, uint32_t 
     return lo;
 }
 
-// Adds the d_out rows of positions [p0, p1) at columns [c, c + 8) onto acc, in
-// order; loads run four rows ahead of the additions.
-template <int DT>
-__device__ __forceinline__ void add_rows(const GradArgs& a, uint32_t p0, uint32_t p1, uint64_t c,
-                                         float (&acc)[8])
-{
-    for (uint32_t p = p0; p < p1; p += 4) {
-        uint4 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (p + u < p1)
-                w[u] = load8<true>(a.d_out + (uint64_t)a.toks[p + u] * a.d_out_pitch, c, a.dim);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (p + u < p1)
-                add8<DT>(acc, w[u]);
-    }
-}
-
-template <int DT, bool VEC>
+// Row v of the gradient at columns [c, c + 8): scale * acc, added onto `old`
+// (that row's values) if ADD.
+template <int DT, bool VEC, bool ADD>
 __device__ __forceinline__ void store_row(const GradArgs& a, uint32_t v, uint64_t c,
-                                          const float (&acc)[8])
+                                          const float (&acc)[8], uint4 old)
 {
-    uint16_t* row = a.d_table + (uint64_t)v * a.table_pitch;
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         x[i] = acc[i] * a.scale;
-    if (a.add)
-        add8<DT>(x, load8<VEC>(row, c, a.dim));
-    store8_row<VEC>(row, c, a.dim, narrow8<DT>(x));
+    if (ADD)
+        add8<DT>(x, old);
+    store8_row<VEC>(a.d_table + (uint64_t)v * a.table_pitch, c, a.dim, narrow8<DT>(x));
 }
 
-// The first CTAs sum whole cells of one number into partial rows; the others
-// take kRowsPerCta table rows each and finish those whose run holds no whole
-// cell.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_embed_rows(const GradArgs a)
+template <bool VEC, bool ADD>
+__device__ __forceinline__ uint4 load_old(const GradArgs& a, uint32_t v, uint64_t c)
 {
-    __shared__ uint32_t start[kRowsPerCta + 1];
-    pdl_entry();
-    if (blockIdx.x < a.cells) {
-        const uint32_t p = blockIdx.x * kRun;
-        if (p + kRun > a.n || a.keys[p] != a.keys[p + kRun - 1] || a.keys[p] >= a.vocab)
-            return;
-        for (uint32_t s = threadIdx.x; s < a.slots; s += kThreads) {
-            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            add_rows<DT>(a, p, p + kRun, (uint64_t)s * 8, acc);
-            float4* part = reinterpret_cast<float4*>(a.parts + ((uint64_t)blockIdx.x * a.slots + s) * 8);
-            part[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            part[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    return ADD ? load8<VEC>(a.d_table + (uint64_t)v * a.table_pitch, c, a.dim) : make_uint4(0, 0, 0, 0);
+}
+
+// Partial rows of a cell: [0] of a run that began before it and ends in it,
+// [1] of one that goes on behind it.
+__device__ __forceinline__ float* part_of(const GradArgs& a, uint32_t cell, uint32_t which, uint32_t slot)
+{
+    return a.parts + (((uint64_t)cell * 2 + which) * a.slots + slot) * 8;
+}
+
+__device__ __forceinline__ void store_part(float* part, const float (&acc)[8])
+{
+    reinterpret_cast<float4*>(part)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    reinterpret_cast<float4*>(part)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+__device__ __forceinline__ void add_part(const float* part, float (&acc)[8])
+{
+    const float4 x = reinterpret_cast<const float4*>(part)[0], y = reinterpret_cast<const float4*>(part)[1];
+    acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+    acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+}
+
+// The runs of one cell, at columns [c, c + 8).  pair: the cell's pairs in shared
+// memory, with those before and after it around them.  BATCH rows of d_out (and,
+// added, the table's rows of the runs that end among them) are loaded ahead.
+template <int DT, bool VEC, bool ADD>
+__device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, uint32_t cell, uint32_t slot)
+{
+    constexpr int BATCH = ADD ? 4 : 8;   // 8 with three CTAs an SM spills
+    const uint64_t c = (uint64_t)slot * 8;
+    uint32_t cur = pair[0].x;
+    if (cur >= a.vocab)
+        return;
+    bool before = pair[-1].x == cur;   // the current run began before the cell
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    uint4 kept = make_uint4(0, 0, 0, 0);   // the table's row of the last run
+    for (int p = 0; p < kCell; p += BATCH) {
+        uint4 w[BATCH], old[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const uint2 at = pair[p + u];
+            if (at.x < a.vocab) {
+                w[u] = load8<true>(a.d_out + (uint64_t)at.y * a.d_out_pitch, c, a.dim);
+                if (ADD && pair[p + u + 1].x != at.x)
+                    old[u] = load_old<VEC, ADD>(a, at.x, c);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const uint32_t key = pair[p + u].x;
+            if (key != cur) {
+                if (before)
+                    store_part(part_of(a, cell, 0, slot), acc);
+                else
+                    store_row<DT, VEC, ADD>(a, cur, c, acc, kept);
+                before = false;
+                cur = key;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[i] = 0.0f;
+            }
+            if (cur >= a.vocab)
+                return;
+            add8<DT>(acc, w[u]);
+            if (ADD)
+                kept = old[u];   // only read if the run ends here
+        }
+    }
+    if (pair[kCell].x == cur)
+        store_part(part_of(a, cell, 1, slot), acc);
+    else if (before)
+        store_part(part_of(a, cell, 0, slot), acc);
+    else
+        store_row<DT, VEC, ADD>(a, cur, c, acc, kept);
+}
+
+// Writes zeros to the rows of absent tokens among kZeroRows rows (a stored
+// gradient's, for batches that k_sort_cluster does not sort), as k_embed_absent
+// does; here the sorted pairs say which tokens there are.
+template <bool VEC>
+__device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
+{
+    __shared__ uint32_t range[2];
+    __shared__ uint32_t present[kZeroRows / 32];
+    const uint32_t nv = min((uint32_t)kZeroRows, a.vocab - v0);
+    const bool bulk = VEC && a.dim % 8 == 0;
+    if (threadIdx.x < kZeroRows / 32)
+        present[threadIdx.x] = 0;
+    for (uint32_t w = threadIdx.x / 32; w < 2; w += blockDim.x / 32) {
+        const uint32_t at = lower_bound_warp(a.pairs, a.n, w ? v0 + nv : v0);
+        if (threadIdx.x % 32 == 0)
+            range[w] = at;
+    }
+    if (bulk) {
+        for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += blockDim.x)
+            static_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    for (uint32_t p = range[0] + threadIdx.x; p < range[1]; p += blockDim.x) {
+        const uint32_t r = a.pairs[p].x - v0;
+        if (p == range[0] || a.pairs[p - 1].x != r + v0)
+            atomicOr(&present[r / 32], 1u << (r % 32));
+    }
+    __syncthreads();
+    if (!bulk) {
+        for (uint32_t r = 0; r < nv; ++r)
+            if (!(present[r / 32] >> (r % 32) & 1))
+                for (uint32_t s = threadIdx.x; s < a.slots; s += blockDim.x)
+                    store8_row<VEC>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch, (uint64_t)s * 8, a.dim,
+                                    make_uint4(0, 0, 0, 0));
         return;
     }
-    const uint32_t v0 = (blockIdx.x - a.cells) * kRowsPerCta;
-    const uint32_t nv = min((uint32_t)kRowsPerCta, a.vocab - v0);
-    if (threadIdx.x < 64) {
-        const uint32_t w = threadIdx.x / 32;
-        const uint32_t at = lower_bound_warp(a.keys, a.n, w ? v0 + nv : v0);
-        if (threadIdx.x % 32 == 0)
-            start[w ? nv : 0] = at;
-    }
-    __syncthreads();
-    const uint32_t lo = start[0], hi = start[nv];
-    __syncthreads();
-    // position p opens the rows after its predecessor's number up to its own
-    for (uint32_t p = lo + threadIdx.x; p <= hi; p += kThreads) {
-        const uint32_t from = p == lo ? 0 : a.keys[p - 1] - v0 + 1;
-        const uint32_t to = p == hi ? nv : a.keys[p] - v0;
-        for (uint32_t v = from; v <= to; ++v)
-            start[v] = p;
-    }
-    __syncthreads();
-    const uint32_t items = nv * a.slots;
-    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
-        const uint32_t v = i / a.slots;
-        const uint64_t c = (uint64_t)(i - v * a.slots) * 8;
-        const uint32_t s = start[v], e = start[v + 1];
-        if (a.add && s == e)
-            continue;
-        const uint32_t cell = (s + kRun - 1) / kRun * kRun;
-        if (cell + kRun <= e)
-            continue;   // k_embed_join's
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        add_rows<DT>(a, s, e, c, acc);
-        store_row<DT, VEC>(a, v0 + v, c, acc);
-    }
+    for (uint32_t r = threadIdx.x; r < nv; r += blockDim.x)
+        if (!(present[r / 32] >> (r % 32) & 1)) {
+            char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch);
+            for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
+                             "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
+                             : "memory");
+        }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
 }
 
-__device__ __forceinline__ bool whole_cell(const GradArgs& a, uint32_t cell, uint32_t key)
+// A CTA sums per_cta cells, a thread 8 columns of one (of one after another
+// where a row has more columns than the CTA has threads for).  CTAs beyond
+// cell_ctas look for absent tokens; the two kinds are dealt alternately, since
+// one mostly reads and the other writes.
+template <int DT, bool VEC, bool ADD>
+__global__ void __launch_bounds__(kThreads, 2) k_embed_cells(const GradArgs a)
 {
-    const uint64_t p = (uint64_t)cell * kRun;
-    return p + kRun <= a.n && a.keys[p] == key && a.keys[p + kRun - 1] == key;
+    __shared__ __align__(16) uint2 pairs[kMaxCells * kCell + 2];
+    pdl_entry();
+    const uint32_t total = gridDim.x;
+    const uint32_t mine = (uint32_t)((uint64_t)blockIdx.x * a.cell_ctas / total);
+    if ((uint32_t)((uint64_t)(blockIdx.x + 1) * a.cell_ctas / total) == mine) {
+        zero_rows<VEC>(a, (blockIdx.x - mine) * kZeroRows, pairs);
+        return;
+    }
+    const uint32_t cell0 = mine * a.per_cta, ncells = min(a.per_cta, a.cells - cell0);
+    for (uint32_t i = threadIdx.x; i < ncells * kCell + 2; i += blockDim.x) {
+        const int64_t p = (int64_t)cell0 * kCell + i - 1;
+        pairs[i] = p >= 0 && p < a.n ? a.pairs[p] : make_uint2(0xFFFFFFFFu, 0);
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < ncells * a.slots; i += blockDim.x) {
+        const uint32_t c = i / a.slots;
+        sum_cell<DT, VEC, ADD>(a, pairs + 1 + c * kCell, cell0 + c, i - c * a.slots);
+    }
 }
 
-// One CTA per cell and 256 columns; the one whose cell is the first whole one
-// of a run joins the run: its head, its whole cells (in 8 slices of
-// consecutive cells) and its tail.
-template <int DT, bool VEC>
+// Adds up the runs that cross cells.  A CTA looks at kJoinCells cells and 256
+// columns, a warp at one cell: if a run begins in it and goes on behind it, the
+// warp adds its partial rows, [1] of every cell but the last and [0] of that.
+// A run of over kLongRun cells is left to the whole CTA, an eighth of it a warp.
+constexpr uint32_t kLongRun = 8;
+template <int DT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const GradArgs a)
 {
-    __shared__ float sums[kJoinSlices][32][9];
-    __shared__ uint32_t run[2];
+    __shared__ float sums[kJoinCells][32][9];
+    __shared__ uint32_t more[kJoinCells];   // cells behind the first of a long run
     pdl_entry();
-    const uint32_t cell = blockIdx.x;
-    const uint32_t p = cell * kRun;
-    if (p + kRun > a.n)
-        return;
-    const uint32_t key = a.keys[p];
-    if (key >= a.vocab || !whole_cell(a, cell, key) || (cell > 0 && whole_cell(a, cell - 1, key)))
-        return;
-    if (threadIdx.x < 64) {
-        const uint32_t w = threadIdx.x / 32;
-        const uint32_t at = lower_bound_warp(a.keys, a.n, key + w);
-        if (threadIdx.x % 32 == 0)
-            run[w] = at;
-    }
-    __syncthreads();
-    const uint32_t s = run[0], e = run[1];
-    const uint32_t ncells = e / kRun - cell;
-    const uint32_t lane = threadIdx.x % 32, slice = threadIdx.x / 32;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t slot = blockIdx.y * 32 + lane;
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (slot < a.slots) {
-        if (slice == 0)
-            add_rows<DT>(a, s, p, (uint64_t)slot * 8, acc);
-        const uint32_t per = (ncells + kJoinSlices - 1) / kJoinSlices;
-        const uint32_t c1 = min(ncells, (slice + 1) * per);
-#pragma unroll 4
-        for (uint32_t k = slice * per; k < c1; ++k) {
-            const float4* part = reinterpret_cast<const float4*>(
-                a.parts + ((uint64_t)(cell + k) * a.slots + slot) * 8);
-            const float4 x = part[0], y = part[1];
-            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+    const uint32_t first = blockIdx.x * kJoinCells, cell = first + warp;
+    const uint32_t end = (cell + 1) * kCell;   // of the cell
+    uint32_t behind = 0;
+    if (end < a.n) {
+        const uint32_t key = a.pairs[end - 1].x, next = a.pairs[end].x;
+        const uint32_t prev = cell ? a.pairs[cell * kCell - 1].x : 0xFFFFFFFFu;
+        if (key < a.vocab && next == key && prev != key) {
+            behind = 1;
+            for (uint32_t c = cell + 1;; c += 32) {   // does the run fill the cell and go on?
+                const uint64_t e = ((uint64_t)c + lane + 1) * kCell;
+                const uint32_t stops = ~__ballot_sync(0xFFFFFFFFu, e < a.n && a.pairs[e].x == key);
+                if (stops) {
+                    behind += __ffs(stops) - 1;
+                    break;
+                }
+                behind += 32;
+            }
         }
-        if (slice == kJoinSlices - 1)
-            add_rows<DT>(a, (cell + ncells) * kRun, e, (uint64_t)slot * 8, acc);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        sums[slice][lane][i] = acc[i];
+    if (lane == 0)
+        more[warp] = behind > kLongRun ? behind : 0;
+    if (behind && behind <= kLongRun && slot < a.slots) {
+        const uint32_t key = a.pairs[end - 1].x;
+        const uint4 old = load_old<VEC, ADD>(a, key, (uint64_t)slot * 8);
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
+        for (uint32_t k = 0; k < behind; ++k)
+            add_part(part_of(a, cell + k, 1, slot), acc);
+        add_part(part_of(a, cell + behind, 0, slot), acc);
+        store_row<DT, VEC, ADD>(a, key, (uint64_t)slot * 8, acc, old);
+    }
     __syncthreads();
-    if (slice != 0 || slot >= a.slots)
-        return;
-#pragma unroll
-    for (int k = 1; k < kJoinSlices; ++k)
+    for (uint32_t r = 0; r < kJoinCells; ++r) {
+        const uint32_t n = more[r];
+        if (n == 0)
+            continue;
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (slot < a.slots) {
+            const uint32_t per = (n + kJoinCells - 1) / kJoinCells;
+            const uint32_t k1 = min(n, (warp + 1) * per);
+#pragma unroll 8
+            for (uint32_t k = warp * per; k < k1; ++k)
+                add_part(part_of(a, first + r + k, 1, slot), acc);
+            if (warp == kJoinCells - 1)
+                add_part(part_of(a, first + r + n, 0, slot), acc);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            acc[i] += sums[k][lane][i];
-    store_row<DT, VEC>(a, key, (uint64_t)slot * 8, acc);
+            sums[warp][lane][i] = acc[i];
+        __syncthreads();
+        if (warp == 0 && slot < a.slots) {
+#pragma unroll
+            for (int k = 1; k < kJoinCells; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[i] += sums[k][lane][i];
+            const uint32_t key = a.pairs[(first + r + 1) * kCell - 1].x;
+            store_row<DT, VEC, ADD>(a, key, (uint64_t)slot * 8, acc,
+                                    load_old<VEC, ADD>(a, key, (uint64_t)slot * 8));
+        }
+        __syncthreads();
+    }
 }
 
 // -- host ------------------------------------------------------------------------------
@@ -416,28 +818,22 @@ uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // Offsets of the gradient's workspace, in bytes.
 struct GradSpace {
-    uint64_t keys[2], toks[2], counts, parts, total;
+    uint64_t pairs[2], counts, parts, total;
     uint32_t tiles, cells, slots;
 };
 
 GradSpace grad_space(uint64_t tokens, uint64_t dim)
 {
     GradSpace g;
-    g.tiles = (uint32_t)((tokens + kTile - 1) / kTile);
-    g.cells = (uint32_t)(tokens / kRun);
+    const bool one_launch = tokens <= kClusterTokens;
+    g.tiles = one_launch ? 0 : (uint32_t)((tokens + kTile - 1) / kTile);
+    g.cells = (uint32_t)((tokens + kCell - 1) / kCell);
     g.slots = (uint32_t)((dim + 7) / 8);
-    uint64_t at = 0;
-    for (int i = 0; i < 2; ++i) {
-        g.keys[i] = at;
-        at += up256(4 * tokens);
-        g.toks[i] = at;
-        at += up256(4 * tokens);
-    }
-    g.counts = at;
-    at += up256((uint64_t)kDigits * g.tiles * 4);
-    g.parts = at;
-    at += (uint64_t)g.cells * g.slots * 32;
-    g.total = at;
+    g.pairs[0] = 0;
+    g.pairs[1] = up256(8 * tokens);
+    g.counts = g.pairs[1] + (one_launch ? 0 : up256(8 * tokens));
+    g.parts = g.counts + up256((uint64_t)kDigits * g.tiles * 4);
+    g.total = g.parts + (uint64_t)g.cells * g.slots * 64;
     return g;
 }
 
@@ -445,15 +841,27 @@ constexpr uint64_t kMaxIndex = 0x7FFFFFFFull;
 // k_embed_join's grid has a row of CTAs per 256 columns.
 constexpr uint64_t kMaxGradCols = 65535ull * 256;
 
-template <int DT, bool VEC>
-cudaError_t launch_sums(const GradArgs& a, void* stream)
+template <int DT, bool VEC, bool ADD>
+cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, void* stream)
 {
-    cudaError_t e = launch_train(k_embed_rows<DT, VEC>, dim3(a.cells + a.row_ctas), kThreads, 0, 1,
-                                 stream, a);
-    if (e == cudaSuccess && a.cells)
-        e = launch_train(k_embed_join<DT, VEC>, dim3(a.cells, (a.slots + 31) / 32), kThreads, 0, 1,
-                         stream, a);
+    const uint32_t work = a.per_cta * a.slots;
+    const uint32_t threads = work < kThreads ? (work + 31) / 32 * 32 : kThreads;
+    cudaError_t e = cudaSuccess;
+    if (a.cell_ctas + zero_ctas)
+        e = launch_train(k_embed_cells<DT, VEC, ADD>, dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
+    if (e == cudaSuccess && a.cells > 1)
+        e = launch_train(k_embed_join<DT, VEC, ADD>,
+                         dim3((a.cells + kJoinCells - 1) / kJoinCells, (a.slots + 31) / 32), kThreads, 0, 1, stream,
+                         a);
     return e;
+}
+
+template <int DT>
+cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, bool vec, bool add, void* stream)
+{
+    if (add)
+        return vec ? launch_sums<DT, true, true>(a, zero_ctas, stream) : launch_sums<DT, false, true>(a, zero_ctas, stream);
+    return vec ? launch_sums<DT, true, false>(a, zero_ctas, stream) : launch_sums<DT, false, false>(a, zero_ctas, stream);
 }
 
 }  // namespace
@@ -555,6 +963,8 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
         return ZERO_OK;
     const uint32_t n = (uint32_t)ids->count;
     const GradSpace g = grad_space(n, d_table->cols);
+    if ((uint64_t)g.cells * g.slots / kThreads + d_table->rows / kZeroRows + 2 > kMaxIndex)
+        return ZERO_ERR_UNSUPPORTED;   // the grid of k_embed_cells
     if (g.total && (!workspace || workspace_bytes < g.total))
         return ZERO_ERR_INVALID_ARG;
     if (!aligned16(workspace))
@@ -577,23 +987,52 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
         return ZERO_OK;
 
     char* ws = static_cast<char*>(workspace);
-    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + g.keys[0]),
-                         reinterpret_cast<uint32_t*>(ws + g.keys[1])};
-    uint32_t* toks[2] = {reinterpret_cast<uint32_t*>(ws + g.toks[0]),
-                         reinterpret_cast<uint32_t*>(ws + g.toks[1])};
+    uint2* pairs[2] = {reinterpret_cast<uint2*>(ws + g.pairs[0]), reinterpret_cast<uint2*>(ws + g.pairs[1])};
     uint32_t* counts = reinterpret_cast<uint32_t*>(ws + g.counts);
     const uint32_t vocab = (uint32_t)d_table->rows;
+    const bool vec = vec_rows(d_table);
     cudaError_t e = cudaSuccess;
     int cur = 0;
-    for (uint32_t shift = 0; n && shift < 32 && (shift == 0 || vocab >> shift); shift += kDigitBits) {
+    if (n && n <= kClusterTokens) {
+        uint32_t bits = 1;
+        while (bits < 32 && vocab >> bits)
+            ++bits;
+        ClusterSort c = {};
+        c.ids = ids->ids;
+        c.out = pairs[0];
+        c.bad = d_bad;
+        c.n = n;
+        c.id_bytes = ids->bytes;
+        c.vocab = vocab;
+        c.passes = (bits + kClusterDigitBits - 1) / kClusterDigitBits;
+        c.bits = (bits + c.passes - 1) / c.passes;
+        const uint32_t items = (n + kClusterCtas * kClusterThreads - 1) / (kClusterCtas * kClusterThreads);
+        e = items <= 1   ? launch_cluster_sort<1>(c, stream)
+            : items <= 2 ? launch_cluster_sort<2>(c, stream)
+            : items <= 4 ? launch_cluster_sort<4>(c, stream)
+                         : launch_cluster_sort<8>(c, stream);
+        if (e == cudaSuccess && !accumulate) {
+            ZeroArgs z = {};
+            z.ids = ids->ids;
+            z.d_table = static_cast<uint16_t*>(d_table->base);
+            z.table_pitch = d_table->pitch;
+            z.dim = d_table->cols;
+            z.n = n;
+            z.id_bytes = ids->bytes;
+            z.vocab = vocab;
+            z.slots = g.slots;
+            e = launch_train(vec ? k_embed_absent<true> : k_embed_absent<false>, dim3(kZeroCtas), kZeroThreads, 0, 1,
+                             stream, z);
+        }
+    }
+    for (uint32_t shift = 0; n > kClusterTokens && e == cudaSuccess && shift < 32 && (shift == 0 || vocab >> shift);
+         shift += kDigitBits) {
         SortArgs s = {};
         s.ids = shift ? nullptr : ids->ids;
-        s.keys = keys[cur];
-        s.toks = toks[cur];
+        s.in = pairs[cur];
         if (shift)
             cur ^= 1;
-        s.keys_out = keys[cur];
-        s.toks_out = toks[cur];
+        s.out = pairs[cur];
         s.counts = counts;
         s.bad = d_bad;
         s.n = n;
@@ -607,13 +1046,12 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
                              (uint32_t)(kDigits * g.tiles));
         if (e == cudaSuccess)
             e = launch_train(k_sort_move, dim3(g.tiles), kThreads, 0, 1, stream, s);
-        if (e != cudaSuccess)
-            return train_status(e);
     }
+    if (e != cudaSuccess)
+        return train_status(e);
     GradArgs a = {};
     a.d_out = static_cast<const uint16_t*>(d_out->base);
-    a.keys = keys[cur];
-    a.toks = toks[cur];
+    a.pairs = pairs[cur];
     a.parts = reinterpret_cast<float*>(ws + g.parts);
     a.d_table = static_cast<uint16_t*>(d_table->base);
     a.d_out_pitch = d_out->pitch;
@@ -623,13 +1061,12 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
     a.vocab = vocab;
     a.slots = g.slots;
     a.cells = g.cells;
-    a.row_ctas = (uint32_t)(((uint64_t)vocab + kRowsPerCta - 1) / kRowsPerCta);
-    a.add = accumulate;
+    a.per_cta = a.slots < (uint32_t)kThreads ? kThreads / a.slots : 1;
+    a.per_cta = a.per_cta < (uint32_t)kMaxCells ? a.per_cta : (uint32_t)kMaxCells;
+    a.cell_ctas = (a.cells + a.per_cta - 1) / a.per_cta;
     a.scale = scale;
-    const bool vec = vec_rows(d_table);
-    if (d_table->dtype == ZERO_F16)
-        e = vec ? launch_sums<ZERO_F16, true>(a, stream) : launch_sums<ZERO_F16, false>(a, stream);
-    else
-        e = vec ? launch_sums<ZERO_BF16, true>(a, stream) : launch_sums<ZERO_BF16, false>(a, stream);
+    const uint32_t zero_ctas = accumulate || (n && n <= kClusterTokens) ? 0 : (uint32_t)(((uint64_t)vocab + kZeroRows - 1) / kZeroRows);
+    e = d_table->dtype == ZERO_F16 ? launch_sums<ZERO_F16>(a, zero_ctas, vec, accumulate != 0, stream)
+                                   : launch_sums<ZERO_BF16>(a, zero_ctas, vec, accumulate != 0, stream);
     return train_status(e);
 }
