@@ -11,7 +11,8 @@ namespace {
 
 // A row is held in registers by a group of G threads (whole warps), V vectors
 // of 8 elements a thread: vector j of thread i covers columns (j*G + i)*8, so
-// four neighbouring lanes hold one block of the checkpoint.
+// four neighbouring lanes hold one block of the checkpoint.  A CTA takes rows
+// in turn and loads the next one while it works on one.
 struct NormShape {
     uint32_t group;   // G
     uint32_t vecs;    // V: 1, 2 or 4
@@ -20,16 +21,27 @@ struct NormShape {
 };
 
 constexpr uint32_t kNormMinThreads = 128;
+constexpr uint32_t kNormGroup = 512;   // most threads of a row of one or two vectors a thread
+constexpr uint32_t kNormWideGroup = 1024;
 
-// The least V whose group fits 256 threads, else 4.
+// One vector a thread as far as kNormGroup threads go, then two, then four.
 NormShape norm_shape(uint64_t cols)
 {
     const uint32_t nv = (uint32_t)((cols + 7) / 8);
-    uint32_t v = 1;
-    while (v < 4 && (nv + v - 1) / v > 256)
-        v *= 2;
+    const uint32_t v = nv <= kNormGroup ? 1 : nv <= 2 * kNormGroup ? 2 : 4;
     const uint32_t g = ((nv + v - 1) / v + 31) / 32 * 32;
     return NormShape{g, v, g >= kNormMinThreads ? 1 : kNormMinThreads / g};
+}
+
+template <int V>
+struct NormLimits {   // threads of a CTA
+    static constexpr int threads = V == 4 ? (int)kNormWideGroup : (int)kNormGroup;
+};
+
+// Resident CTAs an SM that a grid of rows-in-turn CTAs is sized for.
+uint32_t norm_ctas_per_sm(const NormShape& sh, uint32_t threads_per_sm)
+{
+    return sh.threads() < threads_per_sm ? threads_per_sm / sh.threads() : 1;
 }
 
 __device__ __forceinline__ float warp_sum(float x)
@@ -74,77 +86,108 @@ struct NormFwdArgs {
     float eps;
 };
 
-template <int DT>
-__device__ __forceinline__ void load_gain(const uint16_t* gain, bool vec, uint64_t c,
-                                          uint64_t cols, float (&g)[8])
+// One vector of a row, as it is loaded.
+struct FwdRaw {
+    uint4 x, res;
+};
+
+template <int V>
+__device__ __forceinline__ void load_forward(const NormFwdArgs& a, uint64_t row, uint32_t lane, FwdRaw (&r)[V])
 {
-    if (!gain) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            g[i] = 1.0f;
-        return;
+    for (int j = 0; j < V; ++j) {
+        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
+        const bool in = row < a.rows && c < a.cols;
+        r[j].x = in ? load8<true>(a.x + row * a.x_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
+        r[j].res = in && a.res ? load8<true>(a.res + row * a.res_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
     }
-    set8<DT>(g, vec ? load8<true>(gain, c, cols) : load8<false>(gain, c, cols));
 }
 
+// Bound by memory.  16,384 x 4,096 with residual, h, y and checkpoint: 606 MB.
 template <int DT, int V>
-__global__ void __launch_bounds__(1024) k_norm_forward(const NormFwdArgs a)
+__global__ void __launch_bounds__(NormLimits<V>::threads, V == 4 ? 1 : 2) k_norm_forward(const NormFwdArgs a)
 {
-    __shared__ float sums[32];
+    __shared__ float sums[2][32];
     pdl_entry();
     const uint32_t lane = threadIdx.x % a.group;
-    const uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + threadIdx.x / a.group;
-    const bool live = row < a.rows;
-    float s[V][8];
-    float ss = 0.0f;
+    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + threadIdx.x / a.group;
+    const uint64_t hop = (uint64_t)gridDim.x * a.rows_per_cta;
+    uint4 gain[V];   // of this thread's columns, 16-bit
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        set8<DT>(s[j], live ? load8<true>(a.x + row * a.x_pitch, c, a.cols) : make_uint4(0, 0, 0, 0));
-        if (a.res && live)
-            add8<DT>(s[j], load8<true>(a.res + row * a.res_pitch, c, a.cols));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ss += s[j][i] * s[j][i];
+        gain[j] = !a.gain ? make_uint4(0, 0, 0, 0)
+                          : a.gain_vec ? load8<true>(a.gain, c, a.cols) : load8<false>(a.gain, c, a.cols);
     }
-    ss = group_sum(ss, a.group, sums);
-    const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
-    if (live && lane == 0 && a.rstd)
-        a.rstd[row] = rstd;
+    FwdRaw next[V];
+    load_forward<V>(a, row, lane, next);
+    int flip = 0;
+    // the same number of turns in every group of the CTA
+    for (uint64_t r0 = (uint64_t)blockIdx.x * a.rows_per_cta; r0 < a.rows; r0 += hop, row += hop) {
+        const bool live = row < a.rows;
+        float s[V][8];
+        float ss = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        if (a.h && live && c < a.cols)
-            store8_row<true>(a.h + row * a.h_pitch, c, a.cols, narrow8<DT>(s[j]));
-        float xhat[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            xhat[i] = s[j][i] * rstd;
-        if (a.y && live && c < a.cols) {
-            float g[8], y[8];
-            load_gain<DT>(a.gain, a.gain_vec, c, a.cols, g);
+        for (int j = 0; j < V; ++j) {
+            set8<DT>(s[j], next[j].x);
+            if (a.res)
+                add8<DT>(s[j], next[j].res);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                y[i] = xhat[i] * g[i];
-            store8_row<true>(a.y + row * a.y_pitch, c, a.cols, narrow8<DT>(y));
+                ss += s[j][i] * s[j][i];
         }
-        if (a.q) {
-            if (c >= a.cols) {   // past the row's end: not part of its last block
+        if (r0 + hop < a.rows)
+            load_forward<V>(a, row + hop, lane, next);
+        ss = group_sum(ss, a.group, sums[flip]);
+        flip ^= 1;
+        const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
+        if (live && lane == 0 && a.rstd)
+            a.rstd[row] = rstd;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    xhat[i] = 0.0f;
-            } else if (c + 8 > a.cols) {
+        for (int j = 0; j < V; ++j) {
+            const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
+            const bool in = live && c < a.cols;
+            if (a.h && in)
+                store8_row<true>(a.h + row * a.h_pitch, c, a.cols, narrow8<DT>(s[j]));
+            float xhat[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i >= a.cols)
-                        xhat[i] = 0.0f;
+            for (int i = 0; i < 8; ++i)
+                xhat[i] = s[j][i] * rstd;
+            if (a.y && in) {
+                float y[8];
+                if (a.gain) {
+                    set8<DT>(y, gain[j]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[i] *= xhat[i];
+                    store8_row<true>(a.y + row * a.y_pitch, c, a.cols, narrow8<DT>(y));
+                } else {
+                    store8_row<true>(a.y + row * a.y_pitch, c, a.cols, narrow8<DT>(xhat));
+                }
             }
-            uint32_t sc;
-            const uint2 q = act8_pack8<DT>(xhat, sc);
-            if (live && c < a.cols) {
-                store8_q(a.q + row * a.q_pitch, c, a.cols, q);
-                if (c % ZERO_ACT8_BLOCK == 0)
-                    a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] = (uint8_t)sc;
+            if (a.q) {
+                // elements past the row's end are zero: loaded as zero
+                uint32_t sc;
+                uint2 q;
+                if (nonfinite(ss)) {   // the same in the whole group
+                    q = act8_pack8<DT>(xhat, sc);
+                } else {   // |xhat| <= sqrt(cols): far below the exponent's upper limit
+                    float m = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        m = fmaxf(m, fabsf(xhat[i]));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                    sc = act8_scale<DT>(__float_as_uint(m));
+                    const float inv = act8_inverse(sc);
+                    q = make_uint2(act8_pack4(xhat[0], xhat[1], xhat[2], xhat[3], inv),
+                                   act8_pack4(xhat[4], xhat[5], xhat[6], xhat[7], inv));
+                }
+                if (in) {
+                    store8_q(a.q + row * a.q_pitch, c, a.cols, q);
+                    if (c % ZERO_ACT8_BLOCK == 0)
+                        a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] = (uint8_t)sc;
+                }
             }
         }
     }
@@ -153,6 +196,7 @@ __global__ void __launch_bounds__(1024) k_norm_forward(const NormFwdArgs a)
 // Most CTAs of the backward kernel, each of which leaves one partial row of
 // the gain's gradient: 8 CTAs of 128 threads on each of 152 SMs.
 constexpr uint32_t kNormMaxParts = 1216;
+constexpr uint32_t kNormBackThreads = 1024;   // resident threads an SM it is sized for
 
 struct NormBwdArgs {
     const uint16_t* dy;
@@ -169,62 +213,94 @@ struct NormBwdArgs {
     uint32_t gain_vec;
 };
 
-template <int DT, int V>
-__global__ void __launch_bounds__(1024) k_norm_backward(const NormBwdArgs a)
+struct BwdRaw {
+    uint4 dy, dres;
+    uint2 q;
+    uint32_t s;
+};
+
+template <int V>
+__device__ __forceinline__ void load_backward(const NormBwdArgs& a, uint64_t row, uint32_t lane, BwdRaw (&r)[V])
 {
-    __shared__ float sums[2][32];
-    __shared__ float fold[kNormMinThreads * 4 * 8];   // only CTAs of several groups
-    pdl_entry();
-    const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
-    float dg[V][8], g[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        load_gain<DT>(a.gain, a.gain_vec, ((uint64_t)j * a.group + lane) * 8, a.cols, g[j]);
+        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
+        const bool in = row < a.rows && c < a.cols;
+        r[j].dy = in ? load8<true>(a.dy + row * a.dy_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
+        r[j].q = in ? load8_q(a.q + row * a.q_pitch, c, a.cols) : make_uint2(0, 0);
+        r[j].s = in ? a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] : 127;
+        r[j].dres = in && a.dres ? load8<true>(a.dres + row * a.dres_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Bound by memory.  What lies past a row's end is loaded as zero; the sums that
+// a lost block's NaN step makes of it there are not read.
+template <int DT, int V>
+__global__ void __launch_bounds__(NormLimits<V>::threads, V == 1 ? 2 : 1) k_norm_backward(const NormBwdArgs a)
+{
+    __shared__ float sums[2][32];
+    __shared__ float fold[kNormMinThreads * 8];   // only CTAs of several groups, which hold one vector a thread
+    pdl_entry();
+    const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
+    const uint64_t hop = (uint64_t)gridDim.x * a.rows_per_cta;
+    float dg[V][8];
+    uint4 gain[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
+        gain[j] = !a.gain ? make_uint4(0, 0, 0, 0)
+                          : a.gain_vec ? load8<true>(a.gain, c, a.cols) : load8<false>(a.gain, c, a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             dg[j][i] = 0.0f;
     }
+    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + mine;
+    BwdRaw next[V];
+    load_backward<V>(a, row, lane, next);
+    float next_rstd = row < a.rows ? a.rstd[row] : 0.0f;
     int flip = 0;
-    for (uint64_t r0 = (uint64_t)blockIdx.x * a.rows_per_cta; r0 < a.rows;
-         r0 += (uint64_t)gridDim.x * a.rows_per_cta) {
-        const uint64_t row = r0 + mine;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * a.rows_per_cta; r0 < a.rows; r0 += hop, row += hop) {
         const bool live = row < a.rows;
+        const float rstd = next_rstd;
         float u[V][8], xhat[V][8];
+        uint4 dres[V];
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-            const bool in = live && c < a.cols;
-            set8<DT>(u[j], in ? load8<true>(a.dy + row * a.dy_pitch, c, a.cols)
-                              : make_uint4(0, 0, 0, 0));
-            const uint2 q = in ? load8_q(a.q + row * a.q_pitch, c, a.cols) : make_uint2(0, 0);
-            const float step =
-                in ? act8_step(a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK]) : 0.0f;
-            act8_unpack8(q, step, xhat[j]);
+            const float step = act8_step(next[j].s);
+            dres[j] = next[j].dres;
+            act8_whole8(next[j].q, xhat[j]);
+            float g[8];
+            set8<DT>(g, gain[j]);
+            set8<DT>(u[j], next[j].dy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (c + i >= a.cols)
-                    xhat[j][i] = 0.0f;   // the step may be NaN there
-                dg[j][i] += u[j][i] * xhat[j][i];
-                u[j][i] *= g[j][i];
-                dot += u[j][i] * xhat[j][i];
+                xhat[j][i] *= step;
+                const float t = u[j][i] * xhat[j][i];
+                dg[j][i] += t;
+                dot += a.gain ? g[i] * t : t;
+                if (a.gain)
+                    u[j][i] *= g[i];
             }
+        }
+        if (r0 + hop < a.rows) {
+            load_backward<V>(a, row + hop, lane, next);
+            next_rstd = row + hop < a.rows ? a.rstd[row + hop] : 0.0f;
         }
         dot = group_sum(dot, a.group, sums[flip]);
         flip ^= 1;
         if (live) {
-            const float mean = __fdiv_rn(dot, (float)a.cols), rstd = a.rstd[row];
+            const float mean = __fdiv_rn(dot, (float)a.cols) * rstd;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
                 if (c >= a.cols)
                     continue;
                 float r[8];
-                set8<DT>(r, a.dres ? load8<true>(a.dres + row * a.dres_pitch, c, a.cols)
-                                   : make_uint4(0, 0, 0, 0));
+                set8<DT>(r, dres[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    r[i] += rstd * (u[j][i] - xhat[j][i] * mean);
+                    r[i] += rstd * u[j][i] - mean * xhat[j][i];
                 store8_row<true>(a.dx + row * a.dx_pitch, c, a.cols, narrow8<DT>(r));
             }
         }
@@ -261,7 +337,7 @@ __global__ void __launch_bounds__(1024) k_norm_backward(const NormBwdArgs a)
 }
 
 // d_gain[c] = rnd((add ? d_gain[c] : 0) + sum of the parts, in a fixed order).
-constexpr int kFoldSlices = 8;
+constexpr int kFoldSlices = 32;
 template <int DT>
 __global__ void __launch_bounds__(32 * kFoldSlices)
     k_norm_gain(const float* parts, uint32_t nparts, uint64_t part_pitch, uint64_t cols,
@@ -287,13 +363,12 @@ __global__ void __launch_bounds__(32 * kFoldSlices)
 }
 
 template <int DT>
-cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, void* stream)
+cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
 {
-    const dim3 grid((unsigned)((a.rows + sh.rows - 1) / sh.rows));
     switch (sh.vecs) {
-    case 1: return launch_train(k_norm_forward<DT, 1>, grid, sh.threads(), 0, 1, stream, a);
-    case 2: return launch_train(k_norm_forward<DT, 2>, grid, sh.threads(), 0, 1, stream, a);
-    default: return launch_train(k_norm_forward<DT, 4>, grid, sh.threads(), 0, 1, stream, a);
+    case 1: return launch_train(k_norm_forward<DT, 1>, dim3(grid), sh.threads(), 0, 1, stream, a);
+    case 2: return launch_train(k_norm_forward<DT, 2>, dim3(grid), sh.threads(), 0, 1, stream, a);
+    default: return launch_train(k_norm_forward<DT, 4>, dim3(grid), sh.threads(), 0, 1, stream, a);
     }
 }
 
@@ -317,7 +392,7 @@ uint64_t backward_parts(uint64_t rows, const NormShape& sh)
 // -- pack and unpack -------------------------------------------------------------------
 
 constexpr int kPackThreads = 256;
-constexpr int kPackUnroll = 4;
+constexpr int kPackUnroll = 2;
 
 struct PackArgs {
     uint16_t* x;
@@ -325,42 +400,75 @@ struct PackArgs {
     uint8_t* scale;
     uint64_t x_pitch, q_pitch, scale_pitch;
     uint64_t cols;
-    uint32_t slots;   // 8-element slots a row: 4 per block, so a block is 4 neighbouring lanes
+    uint32_t slots;   // 16-element slots a row: 2 per block, so a block is 2 neighbouring lanes
     uint32_t items;   // slots * rows of this launch
 };
 
+// 16 elements of a row from c on, as two vectors.
+struct Half {
+    uint4 lo, hi;
+};
+
+// Bound by memory: 3.03 bytes an element, of which pack writes 1.03 and unpack 2.
 template <int DT>
 __global__ void __launch_bounds__(kPackThreads) k_act_pack(const PackArgs a)
 {
     pdl_entry();
     const uint32_t i0 = blockIdx.x * (kPackThreads * kPackUnroll) + threadIdx.x;
-    uint4 w[kPackUnroll];
+    Half w[kPackUnroll];
+    uint32_t row[kPackUnroll];
+    uint64_t col[kPackUnroll];
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
         const uint32_t i = i0 + u * kPackThreads;
-        w[u] = make_uint4(0, 0, 0, 0);
-        if (i < a.items) {
-            const uint32_t row = i / a.slots;
-            const uint64_t c = (uint64_t)(i - row * a.slots) * 8;
-            if (c < a.cols)
-                w[u] = load8<true>(a.x + row * a.x_pitch, c, a.cols);
+        w[u].lo = w[u].hi = make_uint4(0, 0, 0, 0);
+        row[u] = i / a.slots;
+        col[u] = (uint64_t)(i - row[u] * a.slots) * 16;
+        if (i < a.items && col[u] < a.cols) {
+            const uint16_t* p = a.x + row[u] * a.x_pitch;
+            w[u].lo = load8<true>(p, col[u], a.cols);
+            w[u].hi = load8<true>(p, col[u] + 8, a.cols);
         }
     }
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
-        const uint32_t i = i0 + u * kPackThreads;
-        float x[8];
-        set8<DT>(x, w[u]);
-        uint32_t sc;
-        const uint2 q = act8_pack8<DT>(x, sc);
-        if (i < a.items) {
-            const uint32_t row = i / a.slots;
-            const uint64_t c = (uint64_t)(i - row * a.slots) * 8;
-            if (c < a.cols) {
-                store8_q(a.q + row * a.q_pitch, c, a.cols, q);
-                if (c % ZERO_ACT8_BLOCK == 0)
-                    a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] = (uint8_t)sc;
+        float x[2][8];
+        set8<DT>(x[0], w[u].lo);
+        set8<DT>(x[1], w[u].hi);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = max(m, max(mag_bits(x[0][i]), mag_bits(x[1][i])));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        const uint32_t sc = act8_scale<DT>(m);
+        const float inv = act8_inverse(sc);
+        uint32_t q[4];
+        if (sc < Act8Limits<DT>::hi + 127) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float(&v)[8] = x[k / 2];
+                const int o = k % 2 * 4;
+                q[k] = act8_pack4(v[o], v[o + 1], v[o + 2], v[o + 3], inv);
             }
+        } else {   // held down by the exponent's limit, or lost
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                q[k] = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[k] |= act8_quant(x[k / 2][k % 2 * 4 + i], inv, sc == kAct8Bad) << (8 * i);
+            }
+        }
+        if (i0 + u * kPackThreads < a.items && col[u] < a.cols) {
+            int8_t* p = a.q + row[u] * a.q_pitch;
+            if (col[u] + 16 <= a.cols) {
+                *reinterpret_cast<uint4*>(p + col[u]) = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+                store8_q(p, col[u], a.cols, make_uint2(q[0], q[1]));
+                store8_q(p, col[u] + 8, a.cols, make_uint2(q[2], q[3]));
+            }
+            if (col[u] % ZERO_ACT8_BLOCK == 0)
+                a.scale[row[u] * a.scale_pitch + col[u] / ZERO_ACT8_BLOCK] = (uint8_t)sc;
         }
     }
 }
@@ -370,35 +478,34 @@ __global__ void __launch_bounds__(kPackThreads) k_act_unpack(const PackArgs a)
 {
     pdl_entry();
     const uint32_t i0 = blockIdx.x * (kPackThreads * kPackUnroll) + threadIdx.x;
-    uint2 q[kPackUnroll];
-    uint32_t sc[kPackUnroll];
+    uint4 q[kPackUnroll];
+    uint32_t sc[kPackUnroll], row[kPackUnroll];
+    uint64_t col[kPackUnroll];
 #pragma unroll
     for (int u = 0; u < kPackUnroll; ++u) {
         const uint32_t i = i0 + u * kPackThreads;
-        q[u] = make_uint2(0, 0);
-        sc[u] = 0;
-        if (i < a.items) {
-            const uint32_t row = i / a.slots;
-            const uint64_t c = (uint64_t)(i - row * a.slots) * 8;
-            if (c < a.cols) {
-                q[u] = load8_q(a.q + row * a.q_pitch, c, a.cols);
-                sc[u] = a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK];
+        q[u] = make_uint4(0, 0, 0, 0);
+        sc[u] = 127;
+        row[u] = i / a.slots;
+        col[u] = (uint64_t)(i - row[u] * a.slots) * 16;
+        if (i < a.items && col[u] < a.cols) {
+            const int8_t* p = a.q + row[u] * a.q_pitch;
+            if (col[u] + 16 <= a.cols) {
+                q[u] = *reinterpret_cast<const uint4*>(p + col[u]);
+            } else {
+                const uint2 lo = load8_q(p, col[u], a.cols), hi = load8_q(p, col[u] + 8, a.cols);
+                q[u] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
+            sc[u] = a.scale[row[u] * a.scale_pitch + col[u] / ZERO_ACT8_BLOCK];
         }
     }
 #pragma unroll
-    for (int u = 0; u < kPackUnroll; ++u) {
-        const uint32_t i = i0 + u * kPackThreads;
-        if (i < a.items) {
-            const uint32_t row = i / a.slots;
-            const uint64_t c = (uint64_t)(i - row * a.slots) * 8;
-            if (c < a.cols) {
-                float x[8];
-                act8_unpack8(q[u], act8_step(sc[u]), x);
-                store8_row<true>(a.x + row * a.x_pitch, c, a.cols, narrow8<DT>(x));
-            }
+    for (int u = 0; u < kPackUnroll; ++u)
+        if (i0 + u * kPackThreads < a.items && col[u] < a.cols) {
+            uint16_t* p = a.x + row[u] * a.x_pitch;
+            store8_row<true>(p, col[u], a.cols, act8_values8<DT>(make_uint2(q[u].x, q[u].y), sc[u]));
+            store8_row<true>(p, col[u] + 8, a.cols, act8_values8<DT>(make_uint2(q[u].z, q[u].w), sc[u]));
         }
-    }
 }
 
 // Pack and unpack run in launches of at most 2^30 slots, so that item numbers
@@ -407,7 +514,7 @@ zero_status_t launch_pack(const zero_mat_t* x, const zero_act8_t* c, bool pack, 
 {
     if (x->rows == 0 || x->cols == 0)
         return ZERO_OK;
-    const uint64_t slots = (x->cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK * 4;
+    const uint64_t slots = (x->cols + ZERO_ACT8_BLOCK - 1) / ZERO_ACT8_BLOCK * 2;
     if (slots > (1ull << 30))
         return ZERO_ERR_UNSUPPORTED;
     const uint64_t step = (1ull << 30) / slots;
@@ -533,8 +640,11 @@ extern "C" zero_status_t zero_norm_forward(const zero_mat_t* x, const zero_mat_t
         return st;
 
     const NormShape sh = norm_shape(x->cols);
-    if ((x->rows + sh.rows - 1) / sh.rows > 0x7FFFFFFFull)
-        return ZERO_ERR_UNSUPPORTED;
+    const uint64_t ctas = (x->rows + sh.rows - 1) / sh.rows;
+    const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, 1024);
+    if (room == 0)
+        return ZERO_ERR_CUDA;
+    const uint32_t grid = (uint32_t)(ctas < room ? ctas : room);
     NormFwdArgs a = {};
     a.x = static_cast<const uint16_t*>(x->base);
     a.x_pitch = x->pitch;
@@ -564,8 +674,8 @@ extern "C" zero_status_t zero_norm_forward(const zero_mat_t* x, const zero_mat_t
     a.group = sh.group;
     a.rows_per_cta = sh.rows;
     a.eps = eps;
-    return train_status(x->dtype == ZERO_F16 ? launch_forward<ZERO_F16>(a, sh, stream)
-                                             : launch_forward<ZERO_BF16>(a, sh, stream));
+    return train_status(x->dtype == ZERO_F16 ? launch_forward<ZERO_F16>(a, sh, grid, stream)
+                                             : launch_forward<ZERO_BF16>(a, sh, grid, stream));
 }
 
 extern "C" uint64_t zero_norm_backward_workspace(uint64_t rows, uint64_t cols)
@@ -634,7 +744,7 @@ extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act
     cudaError_t e = cudaSuccess;
     uint32_t grid = 0;
     if (dy->rows) {
-        const uint64_t room = (uint64_t)sm_count() * (2048 / sh.threads());
+        const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, kNormBackThreads);
         if (room == 0)
             return ZERO_ERR_CUDA;
         const uint64_t parts = backward_parts(dy->rows, sh);

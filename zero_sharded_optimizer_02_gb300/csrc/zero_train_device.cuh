@@ -203,13 +203,114 @@ __device__ __forceinline__ uint2 act8_pack8(const float (&x)[8], uint32_t& scale
     return make_uint2(w[0], w[1]);
 }
 
-// The 8 values that 8 bytes of a block with step `step` stand for (fp32, exact).
-__device__ __forceinline__ void act8_unpack8(uint2 q, float step, float (&x)[8])
+// Adds 1.5 * 2^23 to a value of magnitude at most 2^22: the low byte of the sum
+// is that of the nearest whole number (ties to even), two's complement.
+constexpr float kRoundBias = 12582912.0f;
+
+// act8_pack8 for finite values whose exponent k is not held down by its upper
+// limit: then no x / 2^k passes 127 and one multiply-add rounds it.
+__device__ __forceinline__ uint32_t act8_pack4(float a, float b, float c, float d, float inverse)
 {
-    const uint32_t w[2] = {q.x, q.y};
+    const uint32_t lo = __byte_perm(__float_as_uint(fmaf(a, inverse, kRoundBias)),
+                                    __float_as_uint(fmaf(b, inverse, kRoundBias)), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(fmaf(c, inverse, kRoundBias)),
+                                    __float_as_uint(fmaf(d, inverse, kRoundBias)), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+
+// The 8 whole numbers of 8 bytes, as floats.
+__device__ __forceinline__ void act8_whole8(uint2 q, float (&x)[8])
+{
+    const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};   // q + 128
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = (float)(int)(int8_t)(w[i / 4] >> (8 * (i & 3))) * step;
+    for (int i = 0; i < 8; ++i)   // 2^23 + 128 + q, exactly
+        x[i] = __uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7540 | (i & 3))) - 8388736.0f;
+}
+
+__device__ __forceinline__ uint32_t bf2_add(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The step 2^(s - 127) of a scale byte in both halves of a word, in type DT.
+// binary16 holds it for s in [103, 142]; another is kept as the byte itself
+// under a mark (0xFFFF, which no step has), for convert4_wide.
+template <int DT>
+__device__ __forceinline__ uint32_t step2(uint32_t s)
+{
+    if (DT == ZERO_BF16) {
+        const uint32_t h = s == kAct8Bad ? 0x7FC0u : (s ? s << 7 : 0x0040u);
+        return h * 0x10001u;
+    }
+    if (s < 103 || (s > 142 && s != kAct8Bad))
+        return 0xFFFF0000u | s;
+    const uint32_t h = s == kAct8Bad ? 0x7E00u : s >= 113 ? (s - 112) << 10 : 0x0400u >> (113 - s);
+    return h * 0x10001u;
+}
+
+// Four signed bytes times the step, as two words of two 16-bit values.
+// bfloat16: a byte q is (128 + (q & 127)) - (q < 0 ? 256 : 128): 0x43 above the
+// low 7 bits is 128 + them, and the sign bit is the lowest exponent bit that
+// makes 0xC300 (-128) 0xC380 (-256).  binary16: 0x64 above the byte with its
+// sign bit flipped is 1024 + 128 + q.  Every operation is exact.
+template <int DT>
+__device__ __forceinline__ void convert4(uint32_t w, uint32_t step, uint32_t& lo, uint32_t& hi)
+{
+    if (DT == ZERO_BF16) {
+        const uint32_t mag = w & 0x7F7F7F7Fu, sign = w & 0x80808080u;
+        lo = bf2_mul(bf2_add(__byte_perm(mag, 0x43434343u, 0x4140), __byte_perm(sign, 0xC3C3C3C3u, 0x4140)), step);
+        hi = bf2_mul(bf2_add(__byte_perm(mag, 0x43434343u, 0x4342), __byte_perm(sign, 0xC3C3C3C3u, 0x4342)), step);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        lo = h2_mul(h2_sub(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u), step);
+        hi = h2_mul(h2_sub(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u), step);
+    }
+}
+
+// The same in fp32 with one rounding, for steps that binary16 does not hold.
+__device__ __noinline__ uint2 convert4_wide(uint32_t w, uint32_t s)
+{
+    const float step = act8_step(s);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (float)(int)(int8_t)(w >> (8 * i)) * step;
+    return make_uint2(narrow2<ZERO_F16>(v[0], v[1]), narrow2<ZERO_F16>(v[2], v[3]));
+}
+
+// The 8 values that 8 bytes of a block with scale byte s stand for, in type DT.
+template <int DT>
+__device__ __forceinline__ uint4 act8_values8(uint2 q, uint32_t s)
+{
+    const uint32_t step = step2<DT>(s);
+    uint4 r;
+    if (DT == ZERO_F16 && step >> 16 == 0xFFFFu) {
+        const uint2 a = convert4_wide(q.x, s), b = convert4_wide(q.y, s);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    convert4<DT>(q.x, step, r.x, r.y);
+    convert4<DT>(q.y, step, r.z, r.w);
+    return r;
 }
 
 // Bytes [c, c + 8) of a row of `cols` bytes whose byte c lies on an 8-byte

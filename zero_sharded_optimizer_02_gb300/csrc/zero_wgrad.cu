@@ -314,79 +314,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// -- conversion ---------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t bf2_add(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// The step 2^(s - 127) of a scale byte in both halves of a word, in type DT.
-// binary16 holds it for s in [103, 142]; another is kept as the byte itself
-// under a mark (0xFFFF, which no step has), for convert4_wide.
-template <int DT>
-__device__ __forceinline__ uint32_t step2(uint32_t s)
-{
-    if (DT == ZERO_BF16) {
-        const uint32_t h = s == kAct8Bad ? 0x7FC0u : (s ? s << 7 : 0x0040u);
-        return h * 0x10001u;
-    }
-    if (s < 103 || (s > 142 && s != kAct8Bad))
-        return 0xFFFF0000u | s;
-    const uint32_t h = s == kAct8Bad ? 0x7E00u : s >= 113 ? (s - 112) << 10 : 0x0400u >> (113 - s);
-    return h * 0x10001u;
-}
-
-// Four signed bytes times the step, as two words of two 16-bit values.
-// bfloat16: a byte q is (128 + (q & 127)) - (q < 0 ? 256 : 128): 0x43 above the
-// low 7 bits is 128 + them, and the sign bit is the lowest exponent bit that
-// makes 0xC300 (-128) 0xC380 (-256).  binary16: 0x64 above the byte with its
-// sign bit flipped is 1024 + 128 + q.  Every operation is exact.
-template <int DT>
-__device__ __forceinline__ void convert4(uint32_t w, uint32_t step, uint32_t& lo, uint32_t& hi)
-{
-    if (DT == ZERO_BF16) {
-        const uint32_t mag = w & 0x7F7F7F7Fu, sign = w & 0x80808080u;
-        lo = bf2_mul(bf2_add(__byte_perm(mag, 0x43434343u, 0x4140), __byte_perm(sign, 0xC3C3C3C3u, 0x4140)), step);
-        hi = bf2_mul(bf2_add(__byte_perm(mag, 0x43434343u, 0x4342), __byte_perm(sign, 0xC3C3C3C3u, 0x4342)), step);
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        lo = h2_mul(h2_sub(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u), step);
-        hi = h2_mul(h2_sub(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u), step);
-    }
-}
-
-// The same in fp32 with one rounding, for steps that binary16 does not hold.
-__device__ __noinline__ uint2 convert4_wide(uint32_t w, uint32_t s)
-{
-    const float step = act8_step(s);
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = (float)(int)(int8_t)(w >> (8 * i)) * step;
-    return make_uint2(narrow2<ZERO_F16>(v[0], v[1]), narrow2<ZERO_F16>(v[2], v[3]));
-}
-
 struct WgradArgs {
     const int8_t* q;
     const uint8_t* scale;
