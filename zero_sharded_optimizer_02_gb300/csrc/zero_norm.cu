@@ -12,7 +12,15 @@ namespace {
 // A row is held in registers by a group of G threads (whole warps), V vectors
 // of 8 elements a thread: vector j of thread i covers columns (j*G + i)*8, so
 // four neighbouring lanes hold one block of the checkpoint.  A CTA takes rows
-// in turn and loads the next one while it works on one.
+// in turn.  Each thread copies its own pieces of the next row to a ring in
+// shared memory of its own (cp.async: no barrier, no registers).
+//
+// V = 4 where there are rows enough to fill the GPU: what a thread does once a
+// row (the reduction, addresses, the square root) is then spread over 32
+// elements.  With one vector a thread the kernels were bound by issuing
+// instructions (73% of all slots, 59 an element): forward 117 us and backward
+// 113 us at 16,384 x 4,096.  Few rows take V = 1: more threads a row, less
+// latency.
 struct NormShape {
     uint32_t group;   // G
     uint32_t vecs;    // V: 1, 2 or 4
@@ -21,28 +29,27 @@ struct NormShape {
 };
 
 constexpr uint32_t kNormMinThreads = 128;
-constexpr uint32_t kNormGroup = 512;   // most threads of a row of one or two vectors a thread
-constexpr uint32_t kNormWideGroup = 1024;
+constexpr uint32_t kNormGroup = 512;        // most threads of a row of one or two vectors a thread
+constexpr uint32_t kNormWideGroup = 1024;   // and of four
+constexpr uint32_t kNormMidGroup = 256;     // four vectors with registers for two CTAs an SM
+constexpr uint64_t kNormManyRows = 608;     // 4 rows an SM
 
-// One vector a thread as far as kNormGroup threads go, then two, then four.
-NormShape norm_shape(uint64_t cols)
+NormShape norm_shape(uint64_t rows, uint64_t cols)
 {
     const uint32_t nv = (uint32_t)((cols + 7) / 8);
-    const uint32_t v = nv <= kNormGroup ? 1 : nv <= 2 * kNormGroup ? 2 : 4;
+    uint32_t v = nv <= kNormGroup ? 1 : nv <= 2 * kNormGroup ? 2 : 4;
+    if (rows >= kNormManyRows && nv >= 64)
+        v = nv >= 128 ? 4 : v < 2 ? 2 : v;
     const uint32_t g = ((nv + v - 1) / v + 31) / 32 * 32;
     return NormShape{g, v, g >= kNormMinThreads ? 1 : kNormMinThreads / g};
 }
 
-template <int V>
-struct NormLimits {   // threads of a CTA
-    static constexpr int threads = V == 4 ? (int)kNormWideGroup : (int)kNormGroup;
+template <int V, bool WIDE>
+struct NormLimits {
+    static constexpr int threads =
+        V == 4 ? (int)(WIDE ? kNormWideGroup : kNormMidGroup) : (int)kNormGroup;   // of a CTA
+    static constexpr int ahead = V == 1 ? 3 : WIDE ? 0 : 1;                        // rows
 };
-
-// Resident CTAs an SM that a grid of rows-in-turn CTAs is sized for.
-uint32_t norm_ctas_per_sm(const NormShape& sh, uint32_t threads_per_sm)
-{
-    return sh.threads() < threads_per_sm ? threads_per_sm / sh.threads() : 1;
-}
 
 __device__ __forceinline__ float warp_sum(float x)
 {
@@ -80,114 +87,191 @@ struct NormFwdArgs {
     int8_t* q;
     uint8_t* scale;
     uint64_t x_pitch, res_pitch, h_pitch, y_pitch, q_pitch, scale_pitch;
-    uint64_t rows, cols;
-    uint32_t group, rows_per_cta;
+    uint64_t rows;
+    uint32_t cols, group, rows_per_cta;
     uint32_t gain_vec;   // the gain lies on a 16-byte boundary
-    float eps;
+    float eps, inv_cols;
 };
 
-// One vector of a row, as it is loaded.
-struct FwdRaw {
-    uint4 x, res;
-};
+// Elements of vector j of this thread that the row has: 8, fewer at its end, 0
+// past it.  FULL: the group's vectors cover exactly the row.
+template <bool FULL>
+__device__ __forceinline__ uint32_t have(uint32_t c, uint32_t cols)
+{
+    return FULL || c + 8 <= cols ? 8u : c < cols ? cols - c : 0u;
+}
 
+template <bool FULL>
+__device__ __forceinline__ void store_have(uint16_t* p, uint32_t n, uint4 v)
+{
+    if (FULL || n == 8) {
+        *reinterpret_cast<uint4*>(p) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        if (i < n)
+            p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store_have_q(int8_t* p, uint32_t n, uint2 v)
+{
+    if (FULL || n == 8) {
+        *reinterpret_cast<uint2*>(p) = v;
+        return;
+    }
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        if (i < n)
+            p[i] = (int8_t)(w[i / 4] >> (8 * (i & 3)));
+}
+
+// The gain at columns [c, c + 8); it stays in L1.
+template <int DT, bool FULL>
+__device__ __forceinline__ void load_gain(const uint16_t* gain, uint32_t vec, uint32_t c, uint32_t cols, float (&g)[8])
+{
+    if (vec && (FULL || c + 8 <= cols))
+        set8<DT>(g, __ldg(reinterpret_cast<const uint4*>(gain + c)));
+    else
+        set8<DT>(g, load8<false>(gain, c, cols));
+}
+
+// The ring: [stage][array][vector][thread] of 16 bytes.
 template <int V>
-__device__ __forceinline__ void load_forward(const NormFwdArgs& a, uint64_t row, uint32_t lane, FwdRaw (&r)[V])
+__device__ __forceinline__ uint4* ring_at(uint4* ring, int stage, int array, int j)
+{
+    return ring + ((stage * 2 + array) * V + j) * blockDim.x + threadIdx.x;
+}
+
+// Copies this thread's pieces of one row; p, r: the row at its first column.
+template <int V, bool FULL>
+__device__ __forceinline__ void fetch_pair(uint4* ring, int stage, const uint16_t* p, const uint16_t* r, uint32_t group8,
+                                           uint32_t c, uint32_t cols)
 {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        const bool in = row < a.rows && c < a.cols;
-        r[j].x = in ? load8<true>(a.x + row * a.x_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
-        r[j].res = in && a.res ? load8<true>(a.res + row * a.res_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
+        const uint32_t n = 2 * have<FULL>(c + j * group8, cols), o = n ? j * group8 : 0;
+        cp_async16_part(ring_at<V>(ring, stage, 0, j), p + o, n);
+        if (r)
+            cp_async16_part(ring_at<V>(ring, stage, 1, j), r + o, n);
     }
 }
 
-// Bound by memory.  16,384 x 4,096 with residual, h, y and checkpoint: 606 MB.
-template <int DT, int V>
-__global__ void __launch_bounds__(NormLimits<V>::threads, V == 4 ? 1 : 2) k_norm_forward(const NormFwdArgs a)
+// Bound by memory.  16,384 x 4,096 with residual, h, y and checkpoint: 606 MB,
+// 337 of them written (this GPU writes 4.0 TB/s at most).
+template <int DT, int V, bool WIDE, bool FULL>
+__global__ void __launch_bounds__(NormLimits<V, WIDE>::threads, WIDE ? 1 : 2) k_norm_forward(const NormFwdArgs a)
 {
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ float sums[2][32];
+    constexpr int kAhead = NormLimits<V, WIDE>::ahead;
     pdl_entry();
-    const uint32_t lane = threadIdx.x % a.group;
-    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + threadIdx.x / a.group;
+    const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
+    const uint32_t c0 = lane * 8, group8 = a.group * 8;
     const uint64_t hop = (uint64_t)gridDim.x * a.rows_per_cta;
-    uint4 gain[V];   // of this thread's columns, 16-bit
+    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + mine;
+    // the row that is copied next, and its first column of this thread (a thread
+    // wholly past the row's end stays at column 0 and copies nothing)
+    const uint32_t at = have<FULL>(c0, a.cols) ? c0 : 0;
+    uint64_t ahead = row;
+    const uint16_t* px = a.x + row * a.x_pitch + at;
+    const uint16_t* pr = a.res ? a.res + row * a.res_pitch + at : nullptr;
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows)
+            fetch_pair<V, FULL>(ring, stage, px, pr, group8, c0, a.cols);
+        cp_async_commit();
+        ahead += hop;
+        px += hop * a.x_pitch;
+        if (pr)
+            pr += hop * a.res_pitch;
+    };
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        gain[j] = !a.gain ? make_uint4(0, 0, 0, 0)
-                          : a.gain_vec ? load8<true>(a.gain, c, a.cols) : load8<false>(a.gain, c, a.cols);
-    }
-    FwdRaw next[V];
-    load_forward<V>(a, row, lane, next);
-    int flip = 0;
+    for (int k = 0; k < kAhead; ++k)
+        fetch(k);
+    int flip = 0, stage = 0;
     // the same number of turns in every group of the CTA
     for (uint64_t r0 = (uint64_t)blockIdx.x * a.rows_per_cta; r0 < a.rows; r0 += hop, row += hop) {
-        const bool live = row < a.rows;
+        const bool live = row < a.rows;   // the ring of a group past the last row holds any values
+        if (kAhead == 0)
+            fetch(0);
+        cp_async_wait<kAhead ? kAhead - 1 : 0>();
         float s[V][8];
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            set8<DT>(s[j], next[j].x);
-            if (a.res)
-                add8<DT>(s[j], next[j].res);
+            set8<DT>(s[j], *ring_at<V>(ring, stage, 0, j));
+            if (pr)
+                add8<DT>(s[j], *ring_at<V>(ring, stage, 1, j));
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 ss += s[j][i] * s[j][i];
         }
-        if (r0 + hop < a.rows)
-            load_forward<V>(a, row + hop, lane, next);
+        if (kAhead)
+            fetch(stage ? stage - 1 : kAhead);   // the stage that the last row freed
+        stage = stage == kAhead ? 0 : stage + 1;
         ss = group_sum(ss, a.group, sums[flip]);
         flip ^= 1;
-        const float rstd = __frsqrt_rn(__fdiv_rn(ss, (float)a.cols) + a.eps);
+        const float rstd = __frsqrt_rn(ss * a.inv_cols + a.eps);
         if (live && lane == 0 && a.rstd)
             a.rstd[row] = rstd;
+        if (a.h && live) {
+            uint16_t* p = a.h + row * a.h_pitch + c0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-            const bool in = live && c < a.cols;
-            if (a.h && in)
-                store8_row<true>(a.h + row * a.h_pitch, c, a.cols, narrow8<DT>(s[j]));
-            float xhat[8];
+            for (int j = 0; j < V; ++j)
+                store_have<FULL>(p + j * group8, have<FULL>(c0 + j * group8, a.cols), narrow8<DT>(s[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                xhat[i] = s[j][i] * rstd;
-            if (a.y && in) {
-                float y[8];
-                if (a.gain) {
-                    set8<DT>(y, gain[j]);
+                s[j][i] *= rstd;   // xhat
+        if (a.q) {
+            int8_t* p = a.q + row * a.q_pitch + c0;
+            uint8_t* sp = a.scale + row * a.scale_pitch + c0 / ZERO_ACT8_BLOCK;
+            const bool lost = nonfinite(ss);   // the same in the whole group
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] *= xhat[i];
-                    store8_row<true>(a.y + row * a.y_pitch, c, a.cols, narrow8<DT>(y));
-                } else {
-                    store8_row<true>(a.y + row * a.y_pitch, c, a.cols, narrow8<DT>(xhat));
-                }
-            }
-            if (a.q) {
-                // elements past the row's end are zero: loaded as zero
+            for (int j = 0; j < V; ++j) {
+                // elements past the row's end are zero: copied as zero
                 uint32_t sc;
                 uint2 q;
-                if (nonfinite(ss)) {   // the same in the whole group
-                    q = act8_pack8<DT>(xhat, sc);
+                if (lost) {
+                    q = act8_pack8<DT>(s[j], sc);
                 } else {   // |xhat| <= sqrt(cols): far below the exponent's upper limit
                     float m = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        m = fmaxf(m, fabsf(xhat[i]));
+                        m = fmaxf(m, fabsf(s[j][i]));
                     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                     sc = act8_scale<DT>(__float_as_uint(m));
                     const float inv = act8_inverse(sc);
-                    q = make_uint2(act8_pack4(xhat[0], xhat[1], xhat[2], xhat[3], inv),
-                                   act8_pack4(xhat[4], xhat[5], xhat[6], xhat[7], inv));
+                    q = make_uint2(act8_pack4(s[j][0], s[j][1], s[j][2], s[j][3], inv),
+                                   act8_pack4(s[j][4], s[j][5], s[j][6], s[j][7], inv));
                 }
-                if (in) {
-                    store8_q(a.q + row * a.q_pitch, c, a.cols, q);
-                    if (c % ZERO_ACT8_BLOCK == 0)
-                        a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] = (uint8_t)sc;
+                const uint32_t n = have<FULL>(c0 + j * group8, a.cols);
+                if (live && (FULL || n)) {
+                    store_have_q<FULL>(p + j * group8, n, q);
+                    if (lane % 4 == 0)   // group8 is a multiple of the block
+                        sp[j * (group8 / ZERO_ACT8_BLOCK)] = (uint8_t)sc;
                 }
+            }
+        }
+        if (a.y && live) {
+            uint16_t* p = a.y + row * a.y_pitch + c0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const uint32_t c = c0 + j * group8;
+                float g[8];
+                if (a.gain) {
+                    load_gain<DT, FULL>(a.gain, a.gain_vec, c, a.cols, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        s[j][i] *= g[i];
+                }
+                store_have<FULL>(p + j * group8, have<FULL>(c, a.cols), narrow8<DT>(s[j]));
             }
         }
     }
@@ -196,7 +280,6 @@ __global__ void __launch_bounds__(NormLimits<V>::threads, V == 4 ? 1 : 2) k_norm
 // Most CTAs of the backward kernel, each of which leaves one partial row of
 // the gain's gradient: 8 CTAs of 128 threads on each of 152 SMs.
 constexpr uint32_t kNormMaxParts = 1216;
-constexpr uint32_t kNormBackThreads = 1024;   // resident threads an SM it is sized for
 
 struct NormBwdArgs {
     const uint16_t* dy;
@@ -208,113 +291,139 @@ struct NormBwdArgs {
     uint16_t* dx;
     float* parts;        // [gridDim.x][part_pitch], or null: no gain gradient
     uint64_t dy_pitch, q_pitch, scale_pitch, dres_pitch, dx_pitch, part_pitch;
-    uint64_t rows, cols;
-    uint32_t group, rows_per_cta;
+    uint64_t rows;
+    uint32_t cols, group, rows_per_cta;
     uint32_t gain_vec;
+    float inv_cols;
 };
 
-struct BwdRaw {
-    uint4 dy, dres;
-    uint2 q;
-    uint32_t s;
-};
-
-template <int V>
-__device__ __forceinline__ void load_backward(const NormBwdArgs& a, uint64_t row, uint32_t lane, BwdRaw (&r)[V])
+// Bound by memory: 472 MB at 16,384 x 4,096 with a residual's gradient.  What
+// lies past a row's end is copied as zero; the sums that a lost block's NaN step
+// makes of it there are not read.
+template <int DT, int V, bool WIDE, bool FULL>
+__global__ void __launch_bounds__(NormLimits<V, WIDE>::threads, WIDE ? 1 : 2) k_norm_backward(const NormBwdArgs a)
 {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        const bool in = row < a.rows && c < a.cols;
-        r[j].dy = in ? load8<true>(a.dy + row * a.dy_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
-        r[j].q = in ? load8_q(a.q + row * a.q_pitch, c, a.cols) : make_uint2(0, 0);
-        r[j].s = in ? a.scale[row * a.scale_pitch + c / ZERO_ACT8_BLOCK] : 127;
-        r[j].dres = in && a.dres ? load8<true>(a.dres + row * a.dres_pitch, c, a.cols) : make_uint4(0, 0, 0, 0);
-    }
-}
-
-// Bound by memory.  What lies past a row's end is loaded as zero; the sums that
-// a lost block's NaN step makes of it there are not read.
-template <int DT, int V>
-__global__ void __launch_bounds__(NormLimits<V>::threads, V == 1 ? 2 : 1) k_norm_backward(const NormBwdArgs a)
-{
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ float sums[2][32];
-    __shared__ float fold[kNormMinThreads * 8];   // only CTAs of several groups, which hold one vector a thread
+    constexpr int kAhead = NormLimits<V, WIDE>::ahead;
     pdl_entry();
     const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
+    const uint32_t c0 = lane * 8, group8 = a.group * 8;
     const uint64_t hop = (uint64_t)gridDim.x * a.rows_per_cta;
+    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + mine;
     float dg[V][8];
-    uint4 gain[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-        gain[j] = !a.gain ? make_uint4(0, 0, 0, 0)
-                          : a.gain_vec ? load8<true>(a.gain, c, a.cols) : load8<false>(a.gain, c, a.cols);
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             dg[j][i] = 0.0f;
-    }
-    uint64_t row = (uint64_t)blockIdx.x * a.rows_per_cta + mine;
-    BwdRaw next[V];
-    load_backward<V>(a, row, lane, next);
-    float next_rstd = row < a.rows ? a.rstd[row] : 0.0f;
-    int flip = 0;
+    // behind the ring of dy and dres, one of the checkpoint's bytes, 8 a vector
+    uint2* qring = reinterpret_cast<uint2*>(ring + (kAhead + 1) * 2 * V * blockDim.x) + threadIdx.x;
+    const uint32_t at = have<FULL>(c0, a.cols) ? c0 : 0;
+    uint64_t ahead = row;
+    const uint16_t* pd = a.dy + row * a.dy_pitch + at;
+    const uint16_t* pr = a.dres ? a.dres + row * a.dres_pitch + at : nullptr;
+    const int8_t* pq = a.q + row * a.q_pitch + at;
+    const uint8_t* ps = a.scale + row * a.scale_pitch + at / ZERO_ACT8_BLOCK;
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+            fetch_pair<V, FULL>(ring, stage, pd, pr, group8, c0, a.cols);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const uint32_t n = have<FULL>(c0 + j * group8, a.cols);
+                cp_async8_part(qring + (stage * V + j) * blockDim.x, pq + (n ? j * group8 : 0), n);
+            }
+        }
+        cp_async_commit();
+        ahead += hop;
+        pd += hop * a.dy_pitch;
+        pq += hop * a.q_pitch;
+        if (pr)
+            pr += hop * a.dres_pitch;
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        fetch(k);
+    // scale bytes and rstd: one row ahead, in registers
+    uint32_t next_s[V], next_rstd;
+    auto scales = [&](uint64_t r) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            next_s[j] = load_byte(ps + j * (group8 / ZERO_ACT8_BLOCK),
+                                  r < a.rows && have<FULL>(c0 + j * group8, a.cols), 127);
+        next_rstd = load_word(a.rstd + r, r < a.rows, 0);
+        ps += hop * a.scale_pitch;
+    };
+    scales(row);
+    int flip = 0, stage = 0;
     for (uint64_t r0 = (uint64_t)blockIdx.x * a.rows_per_cta; r0 < a.rows; r0 += hop, row += hop) {
         const bool live = row < a.rows;
-        const float rstd = next_rstd;
+        if (kAhead == 0)
+            fetch(0);
+        cp_async_wait<kAhead ? kAhead - 1 : 0>();
+        const float rstd = __uint_as_float(next_rstd);
         float u[V][8], xhat[V][8];
-        uint4 dres[V];
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float step = act8_step(next[j].s);
-            dres[j] = next[j].dres;
-            act8_whole8(next[j].q, xhat[j]);
-            float g[8];
-            set8<DT>(g, gain[j]);
-            set8<DT>(u[j], next[j].dy);
+            const float step = act8_step(next_s[j]);
+            act8_whole8(qring[(stage * V + j) * blockDim.x], xhat[j]);
+            set8<DT>(u[j], *ring_at<V>(ring, stage, 0, j));
+            if (!live)   // the ring holds any values: not to be summed
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    u[j][i] = xhat[j][i] = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 xhat[j][i] *= step;
-                const float t = u[j][i] * xhat[j][i];
-                dg[j][i] += t;
-                dot += a.gain ? g[i] * t : t;
-                if (a.gain)
+                dg[j][i] += u[j][i] * xhat[j][i];
+            }
+            if (a.gain) {
+                float g[8];
+                load_gain<DT, FULL>(a.gain, a.gain_vec, c0 + j * group8, a.cols, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
                     u[j][i] *= g[i];
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dot += u[j][i] * xhat[j][i];
         }
-        if (r0 + hop < a.rows) {
-            load_backward<V>(a, row + hop, lane, next);
-            next_rstd = row + hop < a.rows ? a.rstd[row + hop] : 0.0f;
-        }
+        if (kAhead)
+            fetch(stage ? stage - 1 : kAhead);
+        scales(row + hop);
         dot = group_sum(dot, a.group, sums[flip]);
         flip ^= 1;
         if (live) {
-            const float mean = __fdiv_rn(dot, (float)a.cols) * rstd;
+            const float mean = dot * a.inv_cols * rstd;
+            uint16_t* p = a.dx + row * a.dx_pitch + c0;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
-                if (c >= a.cols)
-                    continue;
                 float r[8];
-                set8<DT>(r, dres[j]);
+                if (pr)
+                    set8<DT>(r, *ring_at<V>(ring, stage, 1, j));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    r[i] += rstd * u[j][i] - mean * xhat[j][i];
-                store8_row<true>(a.dx + row * a.dx_pitch, c, a.cols, narrow8<DT>(r));
+                for (int i = 0; i < 8; ++i) {
+                    const float d = rstd * u[j][i] - mean * xhat[j][i];
+                    r[i] = pr ? r[i] + d : d;
+                }
+                store_have<FULL>(p + j * group8, have<FULL>(c0 + j * group8, a.cols), narrow8<DT>(r));
             }
         }
+        stage = stage == kAhead ? 0 : stage + 1;
     }
     if (!a.parts)
         return;
     if (a.rows_per_cta > 1) {   // fold the groups' sums in group order
-        const uint32_t width = a.group * V * 8;
+        const uint32_t width = group8 * V;
+        float* fold = reinterpret_cast<float*>(ring);   // 32 of the ring's 40 bytes a vector and stage
+        cp_async_wait<0>();
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                fold[mine * width + ((uint32_t)j * a.group + lane) * 8 + i] = dg[j][i];
+                fold[mine * width + j * group8 + c0 + i] = dg[j][i];
         __syncthreads();
         if (mine != 0)
             return;
@@ -323,12 +432,12 @@ __global__ void __launch_bounds__(NormLimits<V>::threads, V == 1 ? 2 : 1) k_norm
             for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dg[j][i] += fold[m * width + ((uint32_t)j * a.group + lane) * 8 + i];
+                    dg[j][i] += fold[m * width + j * group8 + c0 + i];
     }
     float* part = a.parts + blockIdx.x * a.part_pitch;   // part_pitch: cols rounded up to 8
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const uint64_t c = ((uint64_t)j * a.group + lane) * 8;
+        const uint32_t c = c0 + j * group8;
         if (c < a.cols) {
             reinterpret_cast<float4*>(part + c)[0] = make_float4(dg[j][0], dg[j][1], dg[j][2], dg[j][3]);
             reinterpret_cast<float4*>(part + c)[1] = make_float4(dg[j][4], dg[j][5], dg[j][6], dg[j][7]);
@@ -362,25 +471,69 @@ __global__ void __launch_bounds__(32 * kFoldSlices)
     }
 }
 
-template <int DT>
+// Shared memory of a forward (two arrays of 16 bytes a vector) or backward
+// (and one of 8) CTA.
+template <int V, bool WIDE>
+constexpr size_t ring_bytes(uint32_t threads, bool backward)
+{
+    return (size_t)(NormLimits<V, WIDE>::ahead + 1) * V * threads * (backward ? 40 : 32);
+}
+static_assert(ring_bytes<4, true>(kNormWideGroup, true) <= 220 * 1024 && ring_bytes<4, false>(kNormMidGroup, true) <= 104 * 1024 &&
+                  ring_bytes<1, false>(kNormGroup, true) <= 104 * 1024 && ring_bytes<2, false>(kNormGroup, true) <= 104 * 1024,
+              "rings exceed shared memory");
+
+bool norm_full(const NormShape& sh, uint64_t cols) { return (uint64_t)sh.group * sh.vecs * 8 == cols; }
+
+template <int DT, int V, bool WIDE, bool FULL>
 cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
 {
-    switch (sh.vecs) {
-    case 1: return launch_train(k_norm_forward<DT, 1>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    case 2: return launch_train(k_norm_forward<DT, 2>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    default: return launch_train(k_norm_forward<DT, 4>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    }
+    static std::atomic<uint64_t> allowed{0};
+    allow_smem(k_norm_forward<DT, V, WIDE, FULL>, ring_bytes<V, WIDE>(NormLimits<V, WIDE>::threads, false), allowed);
+    return launch_train(k_norm_forward<DT, V, WIDE, FULL>, dim3(grid), sh.threads(),
+                        ring_bytes<V, WIDE>(sh.threads(), false), 1, stream, a);
 }
 
 template <int DT>
-cudaError_t launch_backward(const NormBwdArgs& a, const NormShape& sh, uint32_t grid,
-                            void* stream)
+cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
 {
-    switch (sh.vecs) {
-    case 1: return launch_train(k_norm_backward<DT, 1>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    case 2: return launch_train(k_norm_backward<DT, 2>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    default: return launch_train(k_norm_backward<DT, 4>, dim3(grid), sh.threads(), 0, 1, stream, a);
-    }
+    if (sh.vecs == 1)
+        return launch_forward<DT, 1, false, false>(a, sh, grid, stream);
+    if (sh.vecs == 2)
+        return launch_forward<DT, 2, false, false>(a, sh, grid, stream);
+    if (sh.group > kNormMidGroup)
+        return launch_forward<DT, 4, true, false>(a, sh, grid, stream);
+    return norm_full(sh, a.cols) ? launch_forward<DT, 4, false, true>(a, sh, grid, stream)
+                                 : launch_forward<DT, 4, false, false>(a, sh, grid, stream);
+}
+
+template <int DT, int V, bool WIDE, bool FULL>
+cudaError_t launch_backward(const NormBwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
+{
+    static std::atomic<uint64_t> allowed{0};
+    allow_smem(k_norm_backward<DT, V, WIDE, FULL>, ring_bytes<V, WIDE>(NormLimits<V, WIDE>::threads, true), allowed);
+    return launch_train(k_norm_backward<DT, V, WIDE, FULL>, dim3(grid), sh.threads(),
+                        ring_bytes<V, WIDE>(sh.threads(), true), 1, stream, a);
+}
+
+template <int DT>
+cudaError_t launch_backward(const NormBwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
+{
+    if (sh.vecs == 1)
+        return launch_backward<DT, 1, false, false>(a, sh, grid, stream);
+    if (sh.vecs == 2)
+        return launch_backward<DT, 2, false, false>(a, sh, grid, stream);
+    if (sh.group > kNormMidGroup)
+        return launch_backward<DT, 4, true, false>(a, sh, grid, stream);
+    return norm_full(sh, a.cols) ? launch_backward<DT, 4, false, true>(a, sh, grid, stream)
+                                 : launch_backward<DT, 4, false, false>(a, sh, grid, stream);
+}
+
+// Resident CTAs an SM that a grid is sized for: four vectors a thread take 128
+// registers, so 512 threads; else 1,024.
+uint32_t norm_ctas_per_sm(const NormShape& sh)
+{
+    const uint32_t threads = sh.vecs == 4 && sh.group <= kNormMidGroup ? 512 : 1024;
+    return sh.threads() < threads ? threads / sh.threads() : 1;
 }
 
 uint64_t backward_parts(uint64_t rows, const NormShape& sh)
@@ -639,9 +792,9 @@ extern "C" zero_status_t zero_norm_forward(const zero_mat_t* x, const zero_mat_t
     if (st != ZERO_OK)
         return st;
 
-    const NormShape sh = norm_shape(x->cols);
+    const NormShape sh = norm_shape(x->rows, x->cols);
     const uint64_t ctas = (x->rows + sh.rows - 1) / sh.rows;
-    const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, 1024);
+    const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh);
     if (room == 0)
         return ZERO_ERR_CUDA;
     const uint32_t grid = (uint32_t)(ctas < room ? ctas : room);
@@ -670,7 +823,8 @@ extern "C" zero_status_t zero_norm_forward(const zero_mat_t* x, const zero_mat_t
         a.scale_pitch = checkpoint->scale_pitch;
     }
     a.rows = x->rows;
-    a.cols = x->cols;
+    a.cols = (uint32_t)x->cols;
+    a.inv_cols = (float)(1.0 / (double)x->cols);
     a.group = sh.group;
     a.rows_per_cta = sh.rows;
     a.eps = eps;
@@ -684,7 +838,7 @@ extern "C" uint64_t zero_norm_backward_workspace(uint64_t rows, uint64_t cols)
         return UINT64_MAX;
     if (rows == 0 || cols == 0)
         return 0;
-    return backward_parts(rows, norm_shape(cols)) * ((cols + 7) / 8 * 8) * sizeof(float);
+    return backward_parts(rows, norm_shape(rows, cols)) * ((cols + 7) / 8 * 8) * sizeof(float);
 }
 
 extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act8_t* checkpoint,
@@ -738,13 +892,13 @@ extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act
     if (st != ZERO_OK)
         return st;
 
-    const NormShape sh = norm_shape(dy->cols);
+    const NormShape sh = norm_shape(dy->rows, dy->cols);
     const bool f16 = dy->dtype == ZERO_F16;
     const uint64_t pitch = (dy->cols + 7) / 8 * 8;
     cudaError_t e = cudaSuccess;
     uint32_t grid = 0;
     if (dy->rows) {
-        const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, kNormBackThreads);
+        const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh);
         if (room == 0)
             return ZERO_ERR_CUDA;
         const uint64_t parts = backward_parts(dy->rows, sh);
@@ -768,7 +922,8 @@ extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act
         a.parts = d_gain ? static_cast<float*>(workspace) : nullptr;
         a.part_pitch = pitch;
         a.rows = dy->rows;
-        a.cols = dy->cols;
+        a.cols = (uint32_t)dy->cols;
+        a.inv_cols = (float)(1.0 / (double)dy->cols);
         a.group = sh.group;
         a.rows_per_cta = sh.rows;
         e = f16 ? launch_backward<ZERO_F16>(a, sh, grid, stream)

@@ -132,6 +132,43 @@ __device__ __forceinline__ void store8_row(uint16_t* row, uint64_t c, uint64_t c
             row[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
 }
 
+// Asynchronous copies of 16 or 8 bytes to shared memory, of which the first
+// `bytes` (0: none, src is not touched) come from src and the others are zero.
+__device__ __forceinline__ void cp_async16_part(void* dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async8_part(void* dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+// A word, or a byte, from global memory where `there` says so, else `other`.
+// Nothing here looks at it, as a select after the load would: the load stays in
+// flight until its value is needed.
+__device__ __forceinline__ uint32_t load_word(const void* p, bool there, uint32_t other)
+{
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+                 "@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "=&r"(w)
+                 : "l"(p), "r"((uint32_t)there), "r"(other));
+    return w;
+}
+
+__device__ __forceinline__ uint32_t load_byte(const void* p, bool there, uint32_t other)
+{
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+                 "@p ld.global.nc.u8 %0, [%1];\n\t}"
+                 : "=&r"(w)
+                 : "l"(p), "r"((uint32_t)there), "r"(other));
+    return w;
+}
+
 // -- the 8-bit checkpoint -------------------------------------------------------
 
 // Limits of a block's exponent k (zero_act8_t), by the activations' type.

@@ -327,19 +327,6 @@ struct WgradArgs {
     Plan plan;
 };
 
-// A word from global memory where `there` says so, else any.  Nothing here or in
-// the caller looks at it before it is needed, so that loads for later steps
-// stay in flight.
-__device__ __forceinline__ uint32_t load_word(const void* p, bool there)
-{
-    uint32_t w;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0x7F7F7F7F;\n\t"
-                 "@p ld.global.nc.u32 %0, [%1];\n\t}"
-                 : "=r"(w)
-                 : "l"(p), "r"((uint32_t)there));
-    return w;
-}
-
 // 16 elements of one token and their step: 32 bytes of 16-bit values.
 template <int DT>
 __device__ __forceinline__ void convert_chunk(uint4 q, uint32_t step, uint4& lo, uint4& hi)
@@ -613,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             const uint64_t t0 = (uint64_t)k * kStepT;   // the step's first token
             if (t0 > 0 && t0 + kStepT < a.tokens && a.scale_pitch >= 8) {
-                lo = load_word(p - shift / 8, exist);
-                hi = load_word(p - shift / 8 + 4, exist && shift);
+                lo = load_word(p - shift / 8, exist, 0x7F7F7F7Fu);
+                hi = load_word(p - shift / 8 + 4, exist && shift, 0x7F7F7F7Fu);
                 return;
             }
             const uint64_t t = t0 + half * 32 + lane;
