@@ -29,26 +29,29 @@ struct NormShape {
 };
 
 constexpr uint32_t kNormMinThreads = 128;
-constexpr uint32_t kNormGroup = 512;        // most threads of a row of one or two vectors a thread
-constexpr uint32_t kNormWideGroup = 1024;   // and of four
-constexpr uint32_t kNormMidGroup = 256;     // four vectors with registers for two CTAs an SM
+constexpr uint32_t kNormGroup = 512;        // most threads of a row of one vector a thread
+constexpr uint32_t kNormMidGroup = 256;     // of two, or of four with registers for two CTAs an SM
+constexpr uint32_t kNormWideGroup = 1024;   // of four
 constexpr uint64_t kNormManyRows = 608;     // 4 rows an SM
 
-NormShape norm_shape(uint64_t rows, uint64_t cols)
+NormShape norm_shape(uint64_t rows, uint64_t cols, bool backward)
 {
     const uint32_t nv = (uint32_t)((cols + 7) / 8);
-    uint32_t v = nv <= kNormGroup ? 1 : nv <= 2 * kNormGroup ? 2 : 4;
+    uint32_t v = nv <= kNormGroup ? 1 : 4;
     if (rows >= kNormManyRows && nv >= 64)
-        v = nv >= 128 ? 4 : v < 2 ? 2 : v;
+        v = nv < 128 || (backward && nv <= 2 * kNormMidGroup) ? 2 : 4;
     const uint32_t g = ((nv + v - 1) / v + 31) / 32 * 32;
     return NormShape{g, v, g >= kNormMinThreads ? 1 : kNormMinThreads / g};
 }
 
-template <int V, bool WIDE>
+template <int V, bool WIDE, bool BACK>
 struct NormLimits {
-    static constexpr int threads =
-        V == 4 ? (int)(WIDE ? kNormWideGroup : kNormMidGroup) : (int)kNormGroup;   // of a CTA
-    static constexpr int ahead = V == 1 ? 3 : WIDE ? 0 : 1;                        // rows
+    static constexpr int threads = V == 1 ? (int)kNormGroup : (int)(WIDE ? kNormWideGroup : kNormMidGroup);
+    // CTAs an SM that the registers are limited for.  16,384 x 4,096: forward
+    // 101 us with 2, 98 with 3 (x 1,600: 52, 46); backward 117 with 3, 95 with 2,
+    // 145 with 1 (more than two spill).
+    static constexpr int ctas = WIDE ? 1 : V == 1 || BACK ? 2 : 3;
+    static constexpr int ahead = V == 1 ? 3 : WIDE ? 0 : 1;   // rows
 };
 
 __device__ __forceinline__ float warp_sum(float x)
@@ -163,11 +166,11 @@ __device__ __forceinline__ void fetch_pair(uint4* ring, int stage, const uint16_
 // Bound by memory.  16,384 x 4,096 with residual, h, y and checkpoint: 606 MB,
 // 337 of them written (this GPU writes 4.0 TB/s at most).
 template <int DT, int V, bool WIDE, bool FULL>
-__global__ void __launch_bounds__(NormLimits<V, WIDE>::threads, WIDE ? 1 : 2) k_norm_forward(const NormFwdArgs a)
+__global__ void __launch_bounds__(NormLimits<V, WIDE, false>::threads, NormLimits<V, WIDE, false>::ctas) k_norm_forward(const NormFwdArgs a)
 {
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float sums[2][32];
-    constexpr int kAhead = NormLimits<V, WIDE>::ahead;
+    constexpr int kAhead = NormLimits<V, WIDE, false>::ahead;
     pdl_entry();
     const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const uint32_t c0 = lane * 8, group8 = a.group * 8;
@@ -301,11 +304,11 @@ struct NormBwdArgs {
 // lies past a row's end is copied as zero; the sums that a lost block's NaN step
 // makes of it there are not read.
 template <int DT, int V, bool WIDE, bool FULL>
-__global__ void __launch_bounds__(NormLimits<V, WIDE>::threads, WIDE ? 1 : 2) k_norm_backward(const NormBwdArgs a)
+__global__ void __launch_bounds__(NormLimits<V, WIDE, true>::threads, NormLimits<V, WIDE, true>::ctas) k_norm_backward(const NormBwdArgs a)
 {
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float sums[2][32];
-    constexpr int kAhead = NormLimits<V, WIDE>::ahead;
+    constexpr int kAhead = NormLimits<V, WIDE, true>::ahead;
     pdl_entry();
     const uint32_t lane = threadIdx.x % a.group, mine = threadIdx.x / a.group;
     const uint32_t c0 = lane * 8, group8 = a.group * 8;
@@ -473,13 +476,20 @@ __global__ void __launch_bounds__(32 * kFoldSlices)
 
 // Shared memory of a forward (two arrays of 16 bytes a vector) or backward
 // (and one of 8) CTA.
-template <int V, bool WIDE>
-constexpr size_t ring_bytes(uint32_t threads, bool backward)
+template <int V, bool WIDE, bool BACK>
+constexpr size_t ring_bytes(uint32_t threads)
 {
-    return (size_t)(NormLimits<V, WIDE>::ahead + 1) * V * threads * (backward ? 40 : 32);
+    return (size_t)(NormLimits<V, WIDE, BACK>::ahead + 1) * V * threads * (BACK ? 40 : 32);
 }
-static_assert(ring_bytes<4, true>(kNormWideGroup, true) <= 220 * 1024 && ring_bytes<4, false>(kNormMidGroup, true) <= 104 * 1024 &&
-                  ring_bytes<1, false>(kNormGroup, true) <= 104 * 1024 && ring_bytes<2, false>(kNormGroup, true) <= 104 * 1024,
+template <int V, bool WIDE, bool BACK>
+constexpr bool ring_fits()
+{
+    using L = NormLimits<V, WIDE, BACK>;
+    return ring_bytes<V, WIDE, BACK>(L::threads) * L::ctas <= 220 * 1024;
+}
+static_assert(ring_fits<1, false, false>() && ring_fits<2, false, false>() && ring_fits<4, false, false>() &&
+                  ring_fits<4, true, false>() && ring_fits<1, false, true>() && ring_fits<2, false, true>() &&
+                  ring_fits<4, false, true>() && ring_fits<4, true, true>(),
               "rings exceed shared memory");
 
 bool norm_full(const NormShape& sh, uint64_t cols) { return (uint64_t)sh.group * sh.vecs * 8 == cols; }
@@ -488,9 +498,9 @@ template <int DT, int V, bool WIDE, bool FULL>
 cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
 {
     static std::atomic<uint64_t> allowed{0};
-    allow_smem(k_norm_forward<DT, V, WIDE, FULL>, ring_bytes<V, WIDE>(NormLimits<V, WIDE>::threads, false), allowed);
+    allow_smem(k_norm_forward<DT, V, WIDE, FULL>, (ring_bytes<V, WIDE, false>(NormLimits<V, WIDE, false>::threads)), allowed);
     return launch_train(k_norm_forward<DT, V, WIDE, FULL>, dim3(grid), sh.threads(),
-                        ring_bytes<V, WIDE>(sh.threads(), false), 1, stream, a);
+                        (ring_bytes<V, WIDE, false>(sh.threads())), 1, stream, a);
 }
 
 template <int DT>
@@ -499,7 +509,8 @@ cudaError_t launch_forward(const NormFwdArgs& a, const NormShape& sh, uint32_t g
     if (sh.vecs == 1)
         return launch_forward<DT, 1, false, false>(a, sh, grid, stream);
     if (sh.vecs == 2)
-        return launch_forward<DT, 2, false, false>(a, sh, grid, stream);
+        return norm_full(sh, a.cols) ? launch_forward<DT, 2, false, true>(a, sh, grid, stream)
+                                     : launch_forward<DT, 2, false, false>(a, sh, grid, stream);
     if (sh.group > kNormMidGroup)
         return launch_forward<DT, 4, true, false>(a, sh, grid, stream);
     return norm_full(sh, a.cols) ? launch_forward<DT, 4, false, true>(a, sh, grid, stream)
@@ -510,9 +521,9 @@ template <int DT, int V, bool WIDE, bool FULL>
 cudaError_t launch_backward(const NormBwdArgs& a, const NormShape& sh, uint32_t grid, void* stream)
 {
     static std::atomic<uint64_t> allowed{0};
-    allow_smem(k_norm_backward<DT, V, WIDE, FULL>, ring_bytes<V, WIDE>(NormLimits<V, WIDE>::threads, true), allowed);
+    allow_smem(k_norm_backward<DT, V, WIDE, FULL>, (ring_bytes<V, WIDE, true>(NormLimits<V, WIDE, true>::threads)), allowed);
     return launch_train(k_norm_backward<DT, V, WIDE, FULL>, dim3(grid), sh.threads(),
-                        ring_bytes<V, WIDE>(sh.threads(), true), 1, stream, a);
+                        (ring_bytes<V, WIDE, true>(sh.threads())), 1, stream, a);
 }
 
 template <int DT>
@@ -521,18 +532,19 @@ cudaError_t launch_backward(const NormBwdArgs& a, const NormShape& sh, uint32_t 
     if (sh.vecs == 1)
         return launch_backward<DT, 1, false, false>(a, sh, grid, stream);
     if (sh.vecs == 2)
-        return launch_backward<DT, 2, false, false>(a, sh, grid, stream);
+        return norm_full(sh, a.cols) ? launch_backward<DT, 2, false, true>(a, sh, grid, stream)
+                                     : launch_backward<DT, 2, false, false>(a, sh, grid, stream);
     if (sh.group > kNormMidGroup)
         return launch_backward<DT, 4, true, false>(a, sh, grid, stream);
     return norm_full(sh, a.cols) ? launch_backward<DT, 4, false, true>(a, sh, grid, stream)
                                  : launch_backward<DT, 4, false, false>(a, sh, grid, stream);
 }
 
-// Resident CTAs an SM that a grid is sized for: four vectors a thread take 128
-// registers, so 512 threads; else 1,024.
-uint32_t norm_ctas_per_sm(const NormShape& sh)
+// Resident CTAs an SM that a grid is sized for: NormLimits' threads and ctas.
+uint32_t norm_ctas_per_sm(const NormShape& sh, bool backward)
 {
-    const uint32_t threads = sh.vecs == 4 && sh.group <= kNormMidGroup ? 512 : 1024;
+    const uint32_t threads =
+        sh.vecs == 1 || sh.group > kNormMidGroup ? 1024 : (backward ? 2 : 3) * kNormMidGroup;
     return sh.threads() < threads ? threads / sh.threads() : 1;
 }
 
@@ -792,9 +804,9 @@ extern "C" zero_status_t zero_norm_forward(const zero_mat_t* x, const zero_mat_t
     if (st != ZERO_OK)
         return st;
 
-    const NormShape sh = norm_shape(x->rows, x->cols);
+    const NormShape sh = norm_shape(x->rows, x->cols, false);
     const uint64_t ctas = (x->rows + sh.rows - 1) / sh.rows;
-    const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh);
+    const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, false);
     if (room == 0)
         return ZERO_ERR_CUDA;
     const uint32_t grid = (uint32_t)(ctas < room ? ctas : room);
@@ -838,7 +850,7 @@ extern "C" uint64_t zero_norm_backward_workspace(uint64_t rows, uint64_t cols)
         return UINT64_MAX;
     if (rows == 0 || cols == 0)
         return 0;
-    return backward_parts(rows, norm_shape(rows, cols)) * ((cols + 7) / 8 * 8) * sizeof(float);
+    return backward_parts(rows, norm_shape(rows, cols, true)) * ((cols + 7) / 8 * 8) * sizeof(float);
 }
 
 extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act8_t* checkpoint,
@@ -892,13 +904,13 @@ extern "C" zero_status_t zero_norm_backward(const zero_mat_t* dy, const zero_act
     if (st != ZERO_OK)
         return st;
 
-    const NormShape sh = norm_shape(dy->rows, dy->cols);
+    const NormShape sh = norm_shape(dy->rows, dy->cols, true);
     const bool f16 = dy->dtype == ZERO_F16;
     const uint64_t pitch = (dy->cols + 7) / 8 * 8;
     cudaError_t e = cudaSuccess;
     uint32_t grid = 0;
     if (dy->rows) {
-        const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh);
+        const uint64_t room = (uint64_t)sm_count() * norm_ctas_per_sm(sh, true);
         if (room == 0)
             return ZERO_ERR_CUDA;
         const uint64_t parts = backward_parts(dy->rows, sh);
