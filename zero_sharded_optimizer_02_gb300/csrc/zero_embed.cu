@@ -15,7 +15,7 @@ namespace zero {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLookupUnroll = 4;
+constexpr int kLookupUnroll = 2;
 
 __device__ __forceinline__ int64_t load_id(const void* ids, uint32_t bytes, uint64_t i)
 {
@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 
 constexpr int kCell = 32;        // positions of a cell
 constexpr int kMaxCells = 32;    // cells of one CTA
+constexpr uint32_t kManyCells = 456;   // CTAs of cells: three on each of 152 SMs
 constexpr int kZeroRows = 128;   // table rows of one CTA that looks for absent tokens
 static_assert(kMaxCells * kCell * sizeof(uint2) >= kZeroBytes, "zeros fit where the pairs are");
 constexpr int kJoinCells = kThreads / 32;
@@ -604,10 +605,10 @@ __device__ __forceinline__ void add_part(const float* part, float (&acc)[8])
 // The runs of one cell, at columns [c, c + 8).  pair: the cell's pairs in shared
 // memory, with those before and after it around them.  BATCH rows of d_out (and,
 // added, the table's rows of the runs that end among them) are loaded ahead.
-template <int DT, bool VEC, bool ADD>
+template <int DT, bool VEC, bool ADD, bool MANY>
 __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, uint32_t cell, uint32_t slot)
 {
-    constexpr int BATCH = ADD ? 4 : 8;   // 8 with three CTAs an SM spills
+    constexpr int BATCH = ADD ? 4 : 8;
     const uint64_t c = (uint64_t)slot * 8;
     uint32_t cur = pair[0].x;
     if (cur >= a.vocab)
@@ -615,17 +616,25 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
     bool before = pair[-1].x == cur;   // the current run began before the cell
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     uint4 kept = make_uint4(0, 0, 0, 0);   // the table's row of the last run
+    const bool whole = c + 8 <= a.dim;     // not the ragged end of the rows
     for (int p = 0; p < kCell; p += BATCH) {
         uint4 w[BATCH], old[BATCH];
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const uint2 at = pair[p + u];
-            if (at.x < a.vocab) {
-                w[u] = load8<true>(a.d_out + (uint64_t)at.y * a.d_out_pitch, c, a.dim);
-                if (ADD && pair[p + u + 1].x != at.x)
-                    old[u] = load_old<VEC, ADD>(a, at.x, c);
-            }
+            const uint16_t* from = a.d_out + (uint64_t)at.y * a.d_out_pitch;
+            if (MANY)
+                w[u] = load16_once(from + c, at.x < a.vocab && whole);
+            else if (at.x < a.vocab)
+                w[u] = load8<true>(from, c, a.dim);
+            if (ADD && at.x < a.vocab && pair[p + u + 1].x != at.x)
+                old[u] = load_old<VEC, ADD>(a, at.x, c);
         }
+        if (MANY && !whole)
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                if (pair[p + u].x < a.vocab)
+                    w[u] = load8<true>(a.d_out + (uint64_t)pair[p + u].y * a.d_out_pitch, c, a.dim);
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const uint32_t key = pair[p + u].x;
@@ -708,8 +717,12 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
 // where a row has more columns than the CTA has threads for).  CTAs beyond
 // cell_ctas look for absent tokens; the two kinds are dealt alternately, since
 // one mostly reads and the other writes.
-template <int DT, bool VEC, bool ADD>
-__global__ void __launch_bounds__(kThreads, 2) k_embed_cells(const GradArgs a)
+//
+// MANY: more CTAs of cells than run at once.  They read d_out past L1 and have
+// registers for three CTAs an SM: 65,536 tokens x 1,600 added in 106 us against
+// 121; few are quicker otherwise: 1,021 tokens x 768 in 20 us against 17.
+template <int DT, bool VEC, bool ADD, bool MANY>
+__global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const GradArgs a)
 {
     __shared__ __align__(16) uint2 pairs[kMaxCells * kCell + 2];
     pdl_entry();
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_cells(const GradArgs a)
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < ncells * a.slots; i += blockDim.x) {
         const uint32_t c = i / a.slots;
-        sum_cell<DT, VEC, ADD>(a, pairs + 1 + c * kCell, cell0 + c, i - c * a.slots);
+        sum_cell<DT, VEC, ADD, MANY>(a, pairs + 1 + c * kCell, cell0 + c, i - c * a.slots);
     }
 }
 
@@ -848,7 +861,8 @@ cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, void* stream)
     const uint32_t threads = work < kThreads ? (work + 31) / 32 * 32 : kThreads;
     cudaError_t e = cudaSuccess;
     if (a.cell_ctas + zero_ctas)
-        e = launch_train(k_embed_cells<DT, VEC, ADD>, dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
+        e = launch_train(a.cell_ctas > kManyCells ? k_embed_cells<DT, VEC, ADD, true> : k_embed_cells<DT, VEC, ADD, false>,
+                         dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
     if (e == cudaSuccess && a.cells > 1)
         e = launch_train(k_embed_join<DT, VEC, ADD>,
                          dim3((a.cells + kJoinCells - 1) / kJoinCells, (a.slots + 31) / 32), kThreads, 0, 1, stream,

@@ -159,6 +159,18 @@ __device__ __forceinline__ uint32_t load_word(const void* p, bool there, uint32_
     return w;
 }
 
+// 16 bytes that are read once (not kept in L1), or zeros.
+__device__ __forceinline__ uint4 load16_once(const void* p, bool there)
+{
+    uint4 r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+                 "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+                 : "l"(p), "r"((uint32_t)there));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t load_byte(const void* p, bool there, uint32_t other)
 {
     uint32_t w;
