@@ -277,3 +277,33 @@ def test_definition_of_the_checkpoint():
     assert (int(s), int(q)) == (136, 127)
     q, s = ref.pack(torch.tensor([[float("nan"), 1.0]]), "f16")
     assert int(s) == 255 and not q.any()
+
+
+def test_header_compiles_as_c(tmp_path):
+    """Plain C99 against zero_train.h: the descriptors and a host-only entry point."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "use.c"
+    src.write_text("""
+#include <stdio.h>
+#include "zero_train.h"
+int main(void)
+{
+    zero_mat_t m = {0, 0, 8, 8, ZERO_BF16};
+    zero_act8_t c = {0, 0, 0, 8, 16, 1};
+    zero_ids_t i = {0, 0, 8};
+    printf("%d %d %d %llu %u\\n", (int)zero_act_pack(&m, &c, 0), (int)zero_act_unpack(&c, &m, 0),
+           (int)zero_embed_lookup(&m, &i, 1.0f, &m, 0, 0),
+           (unsigned long long)zero_norm_backward_workspace(10, 64), ZERO_ACT8_BLOCK);
+    return 0;
+}
+""")
+    from zero_sharded_optimizer_02_gb300 import _abi, build
+    build.build()
+    exe = tmp_path / "use"
+    subprocess.check_call(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                           os.path.join(root, "include"), str(src), _abi.LIB_PATH, "-o", str(exe),
+                           "-Wl,-rpath," + os.path.dirname(_abi.LIB_PATH)])
+    out = subprocess.check_output([str(exe)], text=True).split()
+    assert out[:3] == ["0", "0", "0"] and int(out[3]) > 0 and out[4] == "32"
