@@ -595,6 +595,51 @@ def test_other_stream_and_graph():
     assert all(torch.equal(a, b) for a, b in zip(results(), want))
 
 
+def test_calls_in_a_row_share_buffers(monkeypatch):
+    """Calls issued back to back on one stream, alternating inputs and sharing their
+    output and workspace, each give what they give alone: with dependent launches,
+    whose kernels start while the call before still runs, and with plain ones."""
+    g = gen(50)
+    vocab, dim, tokens, outs = 5000, 264, 3000, 520
+    sets = []
+    for k in range(3):
+        ids = torch.randint(0, vocab // (k + 1), (tokens - 500 * k,), generator=g, device=DEV)
+        n = ids.numel()
+        x = act(g, n, dim, "bf16", 1.0, 5.0)
+        sets.append(dict(ids=ids, x=x, dy=act(g, n, dim, "bf16"), dyo=act(g, n, outs, "bf16")))
+    table, dw = (torch.empty(r, dim, dtype=torch.bfloat16, device=DEV) for r in (vocab, outs))
+    dg = torch.empty(dim, dtype=torch.bfloat16, device=DEV)
+    rstd = torch.empty(tokens, device=DEV)
+    store = torch.empty(tokens, dim, dtype=torch.bfloat16, device=DEV)
+    q, s = z.act8_empty(tokens, dim)
+    ws = workspace(max(z.zero_embed_grad_workspace(tokens, vocab, dim),
+                       z.zero_act_weight_grad_workspace(tokens, outs, dim),
+                       z.zero_norm_backward_workspace(tokens, dim)))
+
+    def call(c, copy):
+        n = c["ids"].numel()
+        k, dx = z.act8(q[:n], s[:n]), store[:n]
+        z.zero_norm_forward(z.mat(c["x"]), None, None, 1e-5, None, z.mat(dx), rstd, k)
+        z.zero_act_weight_grad(z.mat(c["dyo"]), k, None, False, z.mat(dw), ws, ws.numel())
+        z.zero_norm_backward(z.mat(c["dy"]), k, rstd, None, None, z.mat(dx), dg, False, ws, ws.numel())
+        z.zero_embed_grad(z.mat(dx), z.ids(c["ids"]), 1.0, False, z.mat(table), ws, ws.numel())
+        return [t.clone() for t in (table, dw, dg)] if copy else None
+
+    alone = []
+    for c in sets:
+        torch.cuda.synchronize()
+        alone.append(call(c, True))
+        torch.cuda.synchronize()
+    for pdl in ("1", "0"):
+        monkeypatch.setenv("ZERO_PDL", pdl)
+        for last in range(3):
+            for i in range(9):
+                call(sets[(last + 1 + i) % 3], False)
+            assert (last + 9) % 3 == last
+            got = call(sets[last], True)
+            assert all(torch.equal(a, b) for a, b in zip(got, alone[last]))
+
+
 def test_rows_far_apart():
     """Rows 4 GB apart: element offsets past 2^32 in every operator."""
     far, rows, cols = 1 << 31, 4, 40

@@ -55,6 +55,9 @@ struct LookupArgs {
     float scale;
 };
 
+// out[t] = scale * table[id]: a thread moves kLookupUnroll vectors of 8 elements,
+// a CTA's of neighbouring columns.  Bound by writing: 32,768 x 1,600 in 31 us,
+// 105 MB written at 3.4 of the 4.0 TB/s that a memset reaches.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupArgs a)
 {
@@ -263,7 +266,9 @@ __global__ void __launch_bounds__(kThreads) k_sort_move(const SortArgs a)
 // digits, adds the counts up over warps and, through the other CTAs' shared
 // memory, over CTAs, and moves every pair to its new place: into the CTA that
 // holds it, or in the last pass to global memory.  The multi-launch passes
-// take about 5 us each for their launches alone.
+// take about 6 us for each of their launches.
+// 65,536 tokens of 50,257 numbers (two passes of 8 bits): 25 us, of which the
+// scattered stores to the other CTAs take 5, ranking 8; 1,021 tokens (one CTA): 7 us.
 constexpr int kClusterCtas = 8;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
@@ -429,6 +434,52 @@ cudaError_t launch_cluster_sort(const ClusterSort& a, void* stream)
     while (ctas < kClusterCtas && ctas * kClusterThreads * I < a.n)
         ctas *= 2;
     return launch_train(k_sort_cluster<I>, dim3(ctas), kClusterThreads, cluster_sort_smem(I), ctas, stream, a);
+}
+
+// Up to kCountTokens tokens are sorted by counting: a pair's place is the number
+// of pairs before it.  A CTA keeps all numbers in shared memory, a warp counts for
+// one token at a time.  Up to there, n^2 comparisons over all SMs take less than
+// the radix passes' barriers: 1,021 tokens 3.6 us against 7.0, 2,048 5.0 against
+// 9, 4,096 10.3 against 10.5.
+constexpr uint32_t kCountTokens = 2048;
+constexpr uint32_t kCountCtas = 304;   // two on each of 152 SMs
+__global__ void __launch_bounds__(kThreads) k_sort_count_all(const ClusterSort a)
+{
+    __shared__ __align__(16) uint32_t keys[kCountTokens];
+    pdl_entry();
+    const uint32_t n4 = (a.n + 3) / 4 * 4;
+    bool bad = false;
+    for (uint32_t t = threadIdx.x; t < n4; t += kThreads * 4) {
+        int64_t id[4];
+        load_ids<4>(a.ids, a.id_bytes, t, kThreads, a.n, id);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t u = t + k * kThreads;
+            if (u < n4)   // past the last token: never before one
+                keys[u] = u >= a.n ? 0xFFFFFFFFu
+                                   : id[k] >= 0 && id[k] < (int64_t)a.vocab ? (uint32_t)id[k] : a.vocab;
+            bad |= id[k] >= (int64_t)a.vocab;
+        }
+    }
+    if (bad && a.bad && blockIdx.x == 0)
+        atomicOr(a.bad, 1u);
+    __syncthreads();
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint32_t t = blockIdx.x * kWarps + threadIdx.x / 32; t < a.n; t += gridDim.x * kWarps) {
+        const uint32_t key = keys[t];
+        uint32_t before = 0;
+#pragma unroll 4
+        for (uint32_t u = lane * 4; u < n4; u += 128) {   // of equal numbers, earlier tokens come first
+            const uint4 k = *reinterpret_cast<const uint4*>(keys + u);
+            before += k.x < key + (u < t);
+            before += k.y < key + (u + 1 < t);
+            before += k.z < key + (u + 2 < t);
+            before += k.w < key + (u + 3 < t);
+        }
+        before = __reduce_add_sync(0xFFFFFFFFu, before);
+        if (lane == 0)
+            a.out[before] = make_uint2(key, t);
+    }
 }
 
 // -- rows of absent tokens ------------------------------------------------------------
@@ -693,24 +744,24 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
             atomicOr(&present[r / 32], 1u << (r % 32));
     }
     __syncthreads();
-    if (!bulk) {
+    if (bulk) {
+        for (uint32_t r = threadIdx.x; r < nv; r += blockDim.x)
+            if (!(present[r / 32] >> (r % 32) & 1)) {
+                char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch);
+                for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
+                                 "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
+                                 : "memory");
+            }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
+    } else {
         for (uint32_t r = 0; r < nv; ++r)
             if (!(present[r / 32] >> (r % 32) & 1))
                 for (uint32_t s = threadIdx.x; s < a.slots; s += blockDim.x)
                     store8_row<VEC>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch, (uint64_t)s * 8, a.dim,
                                     make_uint4(0, 0, 0, 0));
-        return;
     }
-    for (uint32_t r = threadIdx.x; r < nv; r += blockDim.x)
-        if (!(present[r / 32] >> (r % 32) & 1)) {
-            char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch);
-            for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
-                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
-                             "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
-                             : "memory");
-        }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
 }
 
 // A CTA sums per_cta cells, a thread 8 columns of one (of one after another
@@ -744,7 +795,8 @@ __global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const Gr
     }
 }
 
-// Adds up the runs that cross cells.  A CTA looks at kJoinCells cells and 256
+// Adds up the runs that cross cells: 15 us at 65,536 tokens x 1,600, bound by the
+// latency of its few dependent loads.  A CTA looks at kJoinCells cells and 256
 // columns, a warp at one cell: if a run begins in it and goes on behind it, the
 // warp adds its partial rows, [1] of every cell but the last and [0] of that.
 // A run of over kLongRun cells is left to the whole CTA, an eighth of it a warp.
@@ -1021,7 +1073,10 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
         c.passes = (bits + kClusterDigitBits - 1) / kClusterDigitBits;
         c.bits = (bits + c.passes - 1) / c.passes;
         const uint32_t items = (n + kClusterCtas * kClusterThreads - 1) / (kClusterCtas * kClusterThreads);
-        e = items <= 1   ? launch_cluster_sort<1>(c, stream)
+        e = n <= kCountTokens
+                ? launch_train(k_sort_count_all, dim3((n + kWarps - 1) / kWarps < kCountCtas ? (n + kWarps - 1) / kWarps : kCountCtas),
+                               kThreads, 0, 1, stream, c)
+            : items <= 1 ? launch_cluster_sort<1>(c, stream)
             : items <= 2 ? launch_cluster_sort<2>(c, stream)
             : items <= 4 ? launch_cluster_sort<4>(c, stream)
                          : launch_cluster_sort<8>(c, stream);

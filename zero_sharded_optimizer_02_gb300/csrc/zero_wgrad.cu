@@ -1,24 +1,27 @@
 // Weight gradient of a linear layer from an 8-bit checkpoint of its input
 // (sm_103a):  dw[o][i] = gain[i] * sum over t of dy[t][o] * xhat[t][i].
 //
-// A matrix product over the tokens, bound by the tensor cores.  Both operands
-// lie with the tokens as rows, so both are "M-major" / "N-major" for
-// tcgen05.mma: rows of 64 elements (128 bytes), one per token, in the 128-byte
-// swizzle.  Pairs of CTAs (cta_group::2) compute tiles of 256 inputs x 256
-// outputs: a CTA holds 128 of the inputs (the rows of its half of the
-// accumulator) and 128 of the outputs.
+// A matrix product over the tokens, on the tensor cores.  Both operands lie with
+// the tokens as rows, so both are "M-major" / "N-major" for tcgen05.mma: rows of
+// 64 elements (128 bytes), one per token, in the 128-byte swizzle.  Pairs of CTAs
+// (cta_group::2) compute tiles of 256 inputs x 256 outputs: a CTA holds 128 of
+// the inputs (the rows of its half of the accumulator) and 128 of the outputs.
 //   - dy goes from global memory to shared memory by TMA;
-//   - the checkpoint's bytes go to shared memory by TMA too; three pairs of warps
+//   - the checkpoint's bytes go to shared memory by TMA too; two pairs of warps
 //     load its scale bytes and leave the steps beside them.  Three groups of four
-//     warps take the token steps in turn: each turns 16 elements of a token at a time
-//     into 16-bit values (exact: a whole number of 7 bits and sign times a power
-//     of two) and stores them where the tensor cores read them.  The 16-bit matrix that a
-//     separate unpack would write and read back never exists;
+//     warps take the token steps in turn: each turns 16 elements of a token at a
+//     time into 16-bit values (exact: a whole number of 7 bits and sign times a
+//     power of two) and stores them where the tensor cores read them.  The 16-bit
+//     matrix that a separate unpack would write and read back never exists;
 //   - one thread of the pair issues the products; four warps of each CTA drain
 //     finished accumulators (two of 256 columns in tensor memory) while the
 //     next tile is summed.
 // Tiles that would leave pairs idle in the last wave are cut along the tokens
 // into `splits` parts each, whose fp32 sums a second launch adds in order.
+//
+// 16,384 tokens, 4,096 -> 16,384: 1.46 ms, 1.51 PFLOP/s; bound by the
+// shared-memory pipe (92% busy), which carries the operands to the tensor cores,
+// the bytes to the converting warps and their values back.
 //
 // Every wait is bounded.  One that runs out (it never does in a healthy run)
 // ends the kernel's loops and the tiles not finished become NaN, so that the
