@@ -5,7 +5,8 @@
 // and every row of the table is then one contiguous run of the sorted order.
 // Numbers are far from evenly spread: a frequent token takes thousands of rows
 // of d_out, so the work is split evenly over the sorted positions, not over the
-// table's rows: a thread sums 8 columns of a cell of 32 positions, run by run.
+// table's rows: a thread sums 8 columns of a cell of 16 or 32 positions, run by
+// run.
 // A run inside one cell is stored at once; one that crosses cells leaves an
 // fp32 partial row in each, and a second launch adds those up in their order.
 // No atomics: the result does not depend on scheduling.
@@ -573,11 +574,15 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 
 // -- sums -----------------------------------------------------------------------------
 
-constexpr int kCell = 32;        // positions of a cell
-constexpr int kMaxCells = 32;    // cells of one CTA
+// Positions of a cell.  MANY (below): 32, else 16, for more threads and shorter
+// chains of loads: 1,021 tokens x 768 added in 10.9 us against 13.9, 12,572 x
+// 1,728 in 30 against 37, but 65,536 x 1,600 in 117 against 100.
+template <bool MANY>
+constexpr int kCellOf = MANY ? 32 : 16;
+constexpr int kMaxPairs = 1024;  // positions of one CTA
 constexpr uint32_t kManyCells = 456;   // CTAs of cells: three on each of 152 SMs
 constexpr int kZeroRows = 128;   // table rows of one CTA that looks for absent tokens
-static_assert(kMaxCells * kCell * sizeof(uint2) >= kZeroBytes, "zeros fit where the pairs are");
+static_assert(kMaxPairs * sizeof(uint2) >= kZeroBytes, "zeros fit where the pairs are");
 constexpr int kJoinCells = kThreads / 32;
 
 struct GradArgs {
@@ -659,7 +664,7 @@ __device__ __forceinline__ void add_part(const float* part, float (&acc)[8])
 template <int DT, bool VEC, bool ADD, bool MANY>
 __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, uint32_t cell, uint32_t slot)
 {
-    constexpr int BATCH = ADD ? 4 : 8;
+    constexpr int BATCH = ADD ? 4 : 8, kCell = kCellOf<MANY>;
     const uint64_t c = (uint64_t)slot * 8;
     uint32_t cur = pair[0].x;
     if (cur >= a.vocab)
@@ -771,11 +776,12 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
 //
 // MANY: more CTAs of cells than run at once.  They read d_out past L1 and have
 // registers for three CTAs an SM: 65,536 tokens x 1,600 added in 106 us against
-// 121; few are quicker otherwise: 1,021 tokens x 768 in 20 us against 17.
+// 121; few are quicker otherwise: 1,021 tokens x 768 in 14 us against 17 (cells of 32).
 template <int DT, bool VEC, bool ADD, bool MANY>
 __global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const GradArgs a)
 {
-    __shared__ __align__(16) uint2 pairs[kMaxCells * kCell + 2];
+    constexpr int kCell = kCellOf<MANY>;
+    __shared__ __align__(16) uint2 pairs[kMaxPairs + 2];
     pdl_entry();
     const uint32_t total = gridDim.x;
     const uint32_t mine = (uint32_t)((uint64_t)blockIdx.x * a.cell_ctas / total);
@@ -801,9 +807,10 @@ __global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const Gr
 // warp adds its partial rows, [1] of every cell but the last and [0] of that.
 // A run of over kLongRun cells is left to the whole CTA, an eighth of it a warp.
 constexpr uint32_t kLongRun = 8;
-template <int DT, bool VEC, bool ADD>
+template <int DT, bool VEC, bool ADD, bool MANY>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const GradArgs a)
 {
+    constexpr int kCell = kCellOf<MANY>;
     __shared__ float sums[kJoinCells][32][9];
     __shared__ uint32_t more[kJoinCells];   // cells behind the first of a long run
     pdl_entry();
@@ -884,16 +891,29 @@ uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
 // Offsets of the gradient's workspace, in bytes.
 struct GradSpace {
     uint64_t pairs[2], counts, parts, total;
-    uint32_t tiles, cells, slots;
+    uint32_t tiles, slots;
+    bool many;               // more CTAs of 32-position cells than run at once
+    uint32_t cells;
+    uint32_t per_cta;        // cells of one CTA
 };
+
+uint32_t cells_per_cta(uint32_t slots, uint32_t cell)
+{
+    const uint32_t fit = slots && slots < (uint32_t)kThreads ? kThreads / slots : 1;
+    return fit < kMaxPairs / cell ? fit : kMaxPairs / cell;
+}
 
 GradSpace grad_space(uint64_t tokens, uint64_t dim)
 {
     GradSpace g;
     const bool one_launch = tokens <= kClusterTokens;
     g.tiles = one_launch ? 0 : (uint32_t)((tokens + kTile - 1) / kTile);
-    g.cells = (uint32_t)((tokens + kCell - 1) / kCell);
     g.slots = (uint32_t)((dim + 7) / 8);
+    const uint32_t wide = cells_per_cta(g.slots, kCellOf<true>) * kCellOf<true>;
+    g.many = (tokens + wide - 1) / wide > kManyCells;
+    const uint32_t cell = g.many ? kCellOf<true> : kCellOf<false>;
+    g.cells = (uint32_t)((tokens + cell - 1) / cell);
+    g.per_cta = cells_per_cta(g.slots, cell);
     g.pairs[0] = 0;
     g.pairs[1] = up256(8 * tokens);
     g.counts = g.pairs[1] + (one_launch ? 0 : up256(8 * tokens));
@@ -906,28 +926,29 @@ constexpr uint64_t kMaxIndex = 0x7FFFFFFFull;
 // k_embed_join's grid has a row of CTAs per 256 columns.
 constexpr uint64_t kMaxGradCols = 65535ull * 256;
 
-template <int DT, bool VEC, bool ADD>
+template <int DT, bool VEC, bool ADD, bool MANY>
 cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, void* stream)
 {
     const uint32_t work = a.per_cta * a.slots;
     const uint32_t threads = work < kThreads ? (work + 31) / 32 * 32 : kThreads;
     cudaError_t e = cudaSuccess;
     if (a.cell_ctas + zero_ctas)
-        e = launch_train(a.cell_ctas > kManyCells ? k_embed_cells<DT, VEC, ADD, true> : k_embed_cells<DT, VEC, ADD, false>,
-                         dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
+        e = launch_train(k_embed_cells<DT, VEC, ADD, MANY>, dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
     if (e == cudaSuccess && a.cells > 1)
-        e = launch_train(k_embed_join<DT, VEC, ADD>,
+        e = launch_train(k_embed_join<DT, VEC, ADD, MANY>,
                          dim3((a.cells + kJoinCells - 1) / kJoinCells, (a.slots + 31) / 32), kThreads, 0, 1, stream,
                          a);
     return e;
 }
 
-template <int DT>
-cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, bool vec, bool add, void* stream)
+template <int DT, bool VEC>
+cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, bool add, bool many, void* stream)
 {
     if (add)
-        return vec ? launch_sums<DT, true, true>(a, zero_ctas, stream) : launch_sums<DT, false, true>(a, zero_ctas, stream);
-    return vec ? launch_sums<DT, true, false>(a, zero_ctas, stream) : launch_sums<DT, false, false>(a, zero_ctas, stream);
+        return many ? launch_sums<DT, VEC, true, true>(a, zero_ctas, stream)
+                    : launch_sums<DT, VEC, true, false>(a, zero_ctas, stream);
+    return many ? launch_sums<DT, VEC, false, true>(a, zero_ctas, stream)
+                : launch_sums<DT, VEC, false, false>(a, zero_ctas, stream);
 }
 
 }  // namespace
@@ -1130,12 +1151,16 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
     a.vocab = vocab;
     a.slots = g.slots;
     a.cells = g.cells;
-    a.per_cta = a.slots < (uint32_t)kThreads ? kThreads / a.slots : 1;
-    a.per_cta = a.per_cta < (uint32_t)kMaxCells ? a.per_cta : (uint32_t)kMaxCells;
+    a.per_cta = g.per_cta;
     a.cell_ctas = (a.cells + a.per_cta - 1) / a.per_cta;
     a.scale = scale;
     const uint32_t zero_ctas = accumulate || (n && n <= kClusterTokens) ? 0 : (uint32_t)(((uint64_t)vocab + kZeroRows - 1) / kZeroRows);
-    e = d_table->dtype == ZERO_F16 ? launch_sums<ZERO_F16>(a, zero_ctas, vec, accumulate != 0, stream)
-                                   : launch_sums<ZERO_BF16>(a, zero_ctas, vec, accumulate != 0, stream);
+    const bool add = accumulate != 0;
+    if (d_table->dtype == ZERO_F16)
+        e = vec ? launch_sums<ZERO_F16, true>(a, zero_ctas, add, g.many, stream)
+                : launch_sums<ZERO_F16, false>(a, zero_ctas, add, g.many, stream);
+    else
+        e = vec ? launch_sums<ZERO_BF16, true>(a, zero_ctas, add, g.many, stream)
+                : launch_sums<ZERO_BF16, false>(a, zero_ctas, add, g.many, stream);
     return train_status(e);
 }
