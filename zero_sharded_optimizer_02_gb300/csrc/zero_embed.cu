@@ -574,13 +574,24 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 
 // -- sums -----------------------------------------------------------------------------
 
-// Positions of a cell.  MANY (below): 32, else 16, for more threads and shorter
-// chains of loads: 1,021 tokens x 768 added in 10.9 us against 13.9, 12,572 x
-// 1,728 in 30 against 37, but 65,536 x 1,600 in 117 against 100.
-template <bool MANY>
-constexpr int kCellOf = MANY ? 32 : 16;
+// How the sums are laid out.
+//   kFew   cells of 16 positions, d_out read through L1, two CTAs an SM;
+//   kSome  more CTAs of such cells than run at once (kSomeCtas): d_out read past
+//          L1, three CTAs an SM;
+//   kMany  over kManyTokens tokens: cells of 32 too.
+// Smaller cells are more threads and shorter chains of loads, but leave more
+// partial rows to write and join.  As few, some and many, us, added:
+//   1,021 x 768    11, 13, 17       16,384 x 768    30, 26, 29
+//   20,000 x 256   27, 29, 32       20,000 x 1,600  61, 57, 57 (stored)
+//   24,000 x 1,600 61, 56, 53       65,536 x 768    87, 71, 66
+//   65,536 x 256   48, 49, 45       65,536 x 1,600  139, 119, 106
+// Only long batches of narrow rows lose: 24,000 x 256 28, 30, 32.
+enum Layout { kFew, kSome, kMany };
+template <int LAYOUT>
+constexpr int kCellOf = LAYOUT == kMany ? 32 : 16;
 constexpr int kMaxPairs = 1024;  // positions of one CTA
-constexpr uint32_t kManyCells = 456;   // CTAs of cells: three on each of 152 SMs
+constexpr uint32_t kSomeCtas = 456;      // three on each of 152 SMs
+constexpr uint64_t kManyTokens = 20000;
 constexpr int kZeroRows = 128;   // table rows of one CTA that looks for absent tokens
 static_assert(kMaxPairs * sizeof(uint2) >= kZeroBytes, "zeros fit where the pairs are");
 constexpr int kJoinCells = kThreads / 32;
@@ -661,10 +672,10 @@ __device__ __forceinline__ void add_part(const float* part, float (&acc)[8])
 // The runs of one cell, at columns [c, c + 8).  pair: the cell's pairs in shared
 // memory, with those before and after it around them.  BATCH rows of d_out (and,
 // added, the table's rows of the runs that end among them) are loaded ahead.
-template <int DT, bool VEC, bool ADD, bool MANY>
+template <int DT, bool VEC, bool ADD, int LAYOUT>
 __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, uint32_t cell, uint32_t slot)
 {
-    constexpr int BATCH = ADD ? 4 : 8, kCell = kCellOf<MANY>;
+    constexpr int BATCH = ADD ? 4 : 8, kCell = kCellOf<LAYOUT>;
     const uint64_t c = (uint64_t)slot * 8;
     uint32_t cur = pair[0].x;
     if (cur >= a.vocab)
@@ -679,14 +690,14 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
         for (int u = 0; u < BATCH; ++u) {
             const uint2 at = pair[p + u];
             const uint16_t* from = a.d_out + (uint64_t)at.y * a.d_out_pitch;
-            if (MANY)
+            if (LAYOUT != kFew)
                 w[u] = load16_once(from + c, at.x < a.vocab && whole);
             else if (at.x < a.vocab)
                 w[u] = load8<true>(from, c, a.dim);
             if (ADD && at.x < a.vocab && pair[p + u + 1].x != at.x)
                 old[u] = load_old<VEC, ADD>(a, at.x, c);
         }
-        if (MANY && !whole)
+        if (LAYOUT != kFew && !whole)
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
                 if (pair[p + u].x < a.vocab)
@@ -773,14 +784,10 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
 // where a row has more columns than the CTA has threads for).  CTAs beyond
 // cell_ctas look for absent tokens; the two kinds are dealt alternately, since
 // one mostly reads and the other writes.
-//
-// MANY: more CTAs of cells than run at once.  They read d_out past L1 and have
-// registers for three CTAs an SM: 65,536 tokens x 1,600 added in 106 us against
-// 121; few are quicker otherwise: 1,021 tokens x 768 in 14 us against 17 (cells of 32).
-template <int DT, bool VEC, bool ADD, bool MANY>
-__global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const GradArgs a)
+template <int DT, bool VEC, bool ADD, int LAYOUT>
+__global__ void __launch_bounds__(kThreads, LAYOUT == kFew ? 2 : 3) k_embed_cells(const GradArgs a)
 {
-    constexpr int kCell = kCellOf<MANY>;
+    constexpr int kCell = kCellOf<LAYOUT>;
     __shared__ __align__(16) uint2 pairs[kMaxPairs + 2];
     pdl_entry();
     const uint32_t total = gridDim.x;
@@ -797,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const Gr
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < ncells * a.slots; i += blockDim.x) {
         const uint32_t c = i / a.slots;
-        sum_cell<DT, VEC, ADD, MANY>(a, pairs + 1 + c * kCell, cell0 + c, i - c * a.slots);
+        sum_cell<DT, VEC, ADD, LAYOUT>(a, pairs + 1 + c * kCell, cell0 + c, i - c * a.slots);
     }
 }
 
@@ -807,10 +814,10 @@ __global__ void __launch_bounds__(kThreads, MANY ? 3 : 2) k_embed_cells(const Gr
 // warp adds its partial rows, [1] of every cell but the last and [0] of that.
 // A run of over kLongRun cells is left to the whole CTA, an eighth of it a warp.
 constexpr uint32_t kLongRun = 8;
-template <int DT, bool VEC, bool ADD, bool MANY>
+template <int DT, bool VEC, bool ADD, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const GradArgs a)
 {
-    constexpr int kCell = kCellOf<MANY>;
+    constexpr int kCell = kCellOf<LAYOUT>;
     __shared__ float sums[kJoinCells][32][9];
     __shared__ uint32_t more[kJoinCells];   // cells behind the first of a long run
     pdl_entry();
@@ -892,7 +899,7 @@ uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
 struct GradSpace {
     uint64_t pairs[2], counts, parts, total;
     uint32_t tiles, slots;
-    bool many;               // more CTAs of 32-position cells than run at once
+    Layout layout;
     uint32_t cells;
     uint32_t per_cta;        // cells of one CTA
 };
@@ -909,9 +916,9 @@ GradSpace grad_space(uint64_t tokens, uint64_t dim)
     const bool one_launch = tokens <= kClusterTokens;
     g.tiles = one_launch ? 0 : (uint32_t)((tokens + kTile - 1) / kTile);
     g.slots = (uint32_t)((dim + 7) / 8);
-    const uint32_t wide = cells_per_cta(g.slots, kCellOf<true>) * kCellOf<true>;
-    g.many = (tokens + wide - 1) / wide > kManyCells;
-    const uint32_t cell = g.many ? kCellOf<true> : kCellOf<false>;
+    const uint32_t wide = cells_per_cta(g.slots, kCellOf<kSome>) * kCellOf<kSome>;
+    g.layout = tokens > kManyTokens ? kMany : (tokens + wide - 1) / wide > kSomeCtas ? kSome : kFew;
+    const uint32_t cell = g.layout == kMany ? kCellOf<kMany> : kCellOf<kFew>;
     g.cells = (uint32_t)((tokens + cell - 1) / cell);
     g.per_cta = cells_per_cta(g.slots, cell);
     g.pairs[0] = 0;
@@ -926,29 +933,37 @@ constexpr uint64_t kMaxIndex = 0x7FFFFFFFull;
 // k_embed_join's grid has a row of CTAs per 256 columns.
 constexpr uint64_t kMaxGradCols = 65535ull * 256;
 
-template <int DT, bool VEC, bool ADD, bool MANY>
+template <int DT, bool VEC, bool ADD, int LAYOUT>
 cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, void* stream)
 {
     const uint32_t work = a.per_cta * a.slots;
     const uint32_t threads = work < kThreads ? (work + 31) / 32 * 32 : kThreads;
     cudaError_t e = cudaSuccess;
     if (a.cell_ctas + zero_ctas)
-        e = launch_train(k_embed_cells<DT, VEC, ADD, MANY>, dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
+        e = launch_train(k_embed_cells<DT, VEC, ADD, LAYOUT>, dim3(a.cell_ctas + zero_ctas), threads, 0, 1, stream, a);
     if (e == cudaSuccess && a.cells > 1)
-        e = launch_train(k_embed_join<DT, VEC, ADD, MANY>,
+        e = launch_train(k_embed_join<DT, VEC, ADD, LAYOUT>,
                          dim3((a.cells + kJoinCells - 1) / kJoinCells, (a.slots + 31) / 32), kThreads, 0, 1, stream,
                          a);
     return e;
 }
 
-template <int DT, bool VEC>
-cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, bool add, bool many, void* stream)
+template <int DT, bool VEC, bool ADD>
+cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, Layout layout, void* stream)
+{
+    return layout == kFew    ? launch_sums<DT, VEC, ADD, kFew>(a, zero_ctas, stream)
+           : layout == kSome ? launch_sums<DT, VEC, ADD, kSome>(a, zero_ctas, stream)
+                             : launch_sums<DT, VEC, ADD, kMany>(a, zero_ctas, stream);
+}
+
+template <int DT>
+cudaError_t launch_sums(const GradArgs& a, uint32_t zero_ctas, bool vec, bool add, Layout layout, void* stream)
 {
     if (add)
-        return many ? launch_sums<DT, VEC, true, true>(a, zero_ctas, stream)
-                    : launch_sums<DT, VEC, true, false>(a, zero_ctas, stream);
-    return many ? launch_sums<DT, VEC, false, true>(a, zero_ctas, stream)
-                : launch_sums<DT, VEC, false, false>(a, zero_ctas, stream);
+        return vec ? launch_sums<DT, true, true>(a, zero_ctas, layout, stream)
+                   : launch_sums<DT, false, true>(a, zero_ctas, layout, stream);
+    return vec ? launch_sums<DT, true, false>(a, zero_ctas, layout, stream)
+               : launch_sums<DT, false, false>(a, zero_ctas, layout, stream);
 }
 
 }  // namespace
@@ -1156,11 +1171,7 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
     a.scale = scale;
     const uint32_t zero_ctas = accumulate || (n && n <= kClusterTokens) ? 0 : (uint32_t)(((uint64_t)vocab + kZeroRows - 1) / kZeroRows);
     const bool add = accumulate != 0;
-    if (d_table->dtype == ZERO_F16)
-        e = vec ? launch_sums<ZERO_F16, true>(a, zero_ctas, add, g.many, stream)
-                : launch_sums<ZERO_F16, false>(a, zero_ctas, add, g.many, stream);
-    else
-        e = vec ? launch_sums<ZERO_BF16, true>(a, zero_ctas, add, g.many, stream)
-                : launch_sums<ZERO_BF16, false>(a, zero_ctas, add, g.many, stream);
+    e = d_table->dtype == ZERO_F16 ? launch_sums<ZERO_F16>(a, zero_ctas, vec, add, g.layout, stream)
+                                   : launch_sums<ZERO_BF16>(a, zero_ctas, vec, add, g.layout, stream);
     return train_status(e);
 }
