@@ -494,8 +494,7 @@ __global__ void __launch_bounds__(kThreads) k_sort_count_all(const ClusterSort a
 // CTA `me` takes every kZeroCtas-th group of 32 rows, since the rows of absent
 // tokens crowd at one end of a vocabulary sorted by frequency and one SM writes
 // only about 25 bytes a clock.  It marks its tokens by reading all numbers.
-// Rows of whole 16-byte vectors are bulk copies of kZeroBytes zeroed bytes of
-// shared memory, a thread a row; others are stored by a warp each.  All SMs
+// A thread takes a row (zero_row).  All SMs
 // write at most 4.0 TB/s (a memset of 1 GB), 0.6 of what a copy moves.
 constexpr uint32_t kZeroCtas = 128;
 constexpr int kZeroThreads = 1024;
@@ -507,22 +506,36 @@ struct ZeroArgs {
     const void* ids;
     uint16_t* d_table;
     uint64_t table_pitch, dim;
-    uint32_t n, id_bytes, vocab, slots;
+    uint32_t n, id_bytes, vocab;
 };
 
-template <bool VEC>
+// Zeros for row v, by one thread: what of it is whole 16-byte vectors in memory
+// by bulk copies of `zeros` (kZeroBytes of them), the ends by elements.
+__device__ void zero_row(uint16_t* d_table, uint64_t pitch, uint64_t dim, uint32_t v, const void* zeros)
+{
+    uint16_t* row = d_table + (uint64_t)v * pitch;
+    const uint64_t head = min((uint64_t)(0 - (reinterpret_cast<uintptr_t>(row) / 2)) % 8, dim);
+    const uint64_t body = (dim - head) / 8 * 8;
+    for (uint64_t i = 0; i < head; ++i)
+        row[i] = 0;
+    for (uint64_t i = head + body; i < dim; ++i)
+        row[i] = 0;
+    char* to = reinterpret_cast<char*>(row + head);
+    for (uint64_t b = 0; b < 2 * body; b += kZeroBytes)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + b),
+                     "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * body - b))
+                     : "memory");
+}
+
 __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 {
     __shared__ __align__(16) uint32_t zeros[kZeroBytes / 4];
     __shared__ uint32_t marks[kMarkWords];
     pdl_begin(1);
     const uint32_t me = blockIdx.x;
-    const bool bulk = VEC && a.dim % 8 == 0;
-    if (bulk) {
-        for (uint32_t i = threadIdx.x; i < kZeroBytes / 4; i += kZeroThreads)
-            zeros[i] = 0;
-        fence_proxy_async_smem();
-    }
+    for (uint32_t i = threadIdx.x; i < kZeroBytes / 4; i += kZeroThreads)
+        zeros[i] = 0;
+    fence_proxy_async_smem();
     const uint32_t groups = (a.vocab + 31) / 32;
     const uint32_t mine = me < groups ? (groups - 1 - me) / kZeroCtas + 1 : 0;   // groups of this CTA
     for (uint32_t lo = 0; lo < mine; lo += kMarkWords) {
@@ -543,32 +556,15 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
         }
         __syncthreads();
         // row 32 ((lo + i) kZeroCtas + me) + bit for word i of the marks
-        if (bulk) {
-            for (uint32_t r = threadIdx.x; r < n * 32; r += kZeroThreads) {
-                const uint32_t v = ((lo + r / 32) * kZeroCtas + me) * 32 + r % 32;
-                if (v < a.vocab && !(marks[r / 32] >> (r % 32) & 1)) {
-                    char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)v * a.table_pitch);
-                    for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
-                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
-                                     "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
-                                     : "memory");
-                }
-            }
-        } else {
-            for (uint32_t r = threadIdx.x / 32; r < n * 32; r += kZeroThreads / 32) {
-                const uint32_t v = ((lo + r / 32) * kZeroCtas + me) * 32 + r % 32;
-                if (v < a.vocab && !(marks[r / 32] >> (r % 32) & 1))
-                    for (uint32_t s = threadIdx.x % 32; s < a.slots; s += 32)
-                        store8_row<VEC>(a.d_table + (uint64_t)v * a.table_pitch, (uint64_t)s * 8, a.dim,
-                                        make_uint4(0, 0, 0, 0));
-            }
+        for (uint32_t r = threadIdx.x; r < n * 32; r += kZeroThreads) {
+            const uint32_t v = ((lo + r / 32) * kZeroCtas + me) * 32 + r % 32;
+            if (v < a.vocab && !(marks[r / 32] >> (r % 32) & 1))
+                zero_row(a.d_table, a.table_pitch, a.dim, v, zeros);
         }
         __syncthreads();
     }
-    if (bulk) {   // the copies read shared memory: not to be left in flight
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
     pdl_end(1);
 }
 
@@ -734,13 +730,11 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
 // Writes zeros to the rows of absent tokens among kZeroRows rows (a stored
 // gradient's, for batches that k_sort_cluster does not sort), as k_embed_absent
 // does; here the sorted pairs say which tokens there are.
-template <bool VEC>
 __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
 {
     __shared__ uint32_t range[2];
     __shared__ uint32_t present[kZeroRows / 32];
     const uint32_t nv = min((uint32_t)kZeroRows, a.vocab - v0);
-    const bool bulk = VEC && a.dim % 8 == 0;
     if (threadIdx.x < kZeroRows / 32)
         present[threadIdx.x] = 0;
     for (uint32_t w = threadIdx.x / 32; w < 2; w += blockDim.x / 32) {
@@ -748,11 +742,9 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
         if (threadIdx.x % 32 == 0)
             range[w] = at;
     }
-    if (bulk) {
-        for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += blockDim.x)
-            static_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-    }
+    for (uint32_t i = threadIdx.x; i < kZeroBytes / 16; i += blockDim.x)
+        static_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
     __syncthreads();
     for (uint32_t p = range[0] + threadIdx.x; p < range[1]; p += blockDim.x) {
         const uint32_t r = a.pairs[p].x - v0;
@@ -760,24 +752,11 @@ __device__ void zero_rows(const GradArgs& a, uint32_t v0, void* zeros)
             atomicOr(&present[r / 32], 1u << (r % 32));
     }
     __syncthreads();
-    if (bulk) {
-        for (uint32_t r = threadIdx.x; r < nv; r += blockDim.x)
-            if (!(present[r / 32] >> (r % 32) & 1)) {
-                char* row = reinterpret_cast<char*>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch);
-                for (uint64_t b = 0; b < 2 * a.dim; b += kZeroBytes)
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(row + b),
-                                 "r"(smem_u32(zeros)), "r"((uint32_t)min((uint64_t)kZeroBytes, 2 * a.dim - b))
-                                 : "memory");
-            }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
-    } else {
-        for (uint32_t r = 0; r < nv; ++r)
-            if (!(present[r / 32] >> (r % 32) & 1))
-                for (uint32_t s = threadIdx.x; s < a.slots; s += blockDim.x)
-                    store8_row<VEC>(a.d_table + (uint64_t)(v0 + r) * a.table_pitch, (uint64_t)s * 8, a.dim,
-                                    make_uint4(0, 0, 0, 0));
-    }
+    for (uint32_t r = threadIdx.x; r < nv; r += blockDim.x)
+        if (!(present[r / 32] >> (r % 32) & 1))
+            zero_row(a.d_table, a.table_pitch, a.dim, v0 + r, zeros);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the copies read shared memory
 }
 
 // A CTA sums per_cta cells, a thread 8 columns of one (of one after another
@@ -793,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, LAYOUT == kFew ? 2 : 3) k_embed_cell
     const uint32_t total = gridDim.x;
     const uint32_t mine = (uint32_t)((uint64_t)blockIdx.x * a.cell_ctas / total);
     if ((uint32_t)((uint64_t)(blockIdx.x + 1) * a.cell_ctas / total) == mine) {
-        zero_rows<VEC>(a, (blockIdx.x - mine) * kZeroRows, pairs);
+        zero_rows(a, (blockIdx.x - mine) * kZeroRows, pairs);
         return;
     }
     const uint32_t cell0 = mine * a.per_cta, ncells = min(a.per_cta, a.cells - cell0);
@@ -1125,9 +1104,7 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
             z.n = n;
             z.id_bytes = ids->bytes;
             z.vocab = vocab;
-            z.slots = g.slots;
-            e = launch_train(vec ? k_embed_absent<true> : k_embed_absent<false>, dim3(kZeroCtas), kZeroThreads, 0, 1,
-                             stream, z);
+            e = launch_train(k_embed_absent, dim3(kZeroCtas), kZeroThreads, 0, 1, stream, z);
         }
     }
     for (uint32_t shift = 0; n > kClusterTokens && e == cudaSuccess && shift < 32 && (shift == 0 || vocab >> shift);
