@@ -16,7 +16,10 @@ namespace zero {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kLookupUnroll = 2;
+// Vectors of a lookup's thread.  32,768 x 1,600 in 31 us with 2, 34 with 1, 32 with
+// 4; of a table whose rows start on any element 39, 37 and 43.
+template <bool VEC>
+constexpr int kLookupUnroll = VEC ? 2 : 1;
 
 __device__ __forceinline__ int64_t load_id(const void* ids, uint32_t bytes, uint64_t i)
 {
@@ -56,17 +59,18 @@ struct LookupArgs {
     float scale;
 };
 
-// out[t] = scale * table[id]: a thread moves kLookupUnroll vectors of 8 elements,
+// out[t] = scale * table[id]: a thread moves kUnroll vectors of 8 elements,
 // a CTA's of neighbouring columns.  Bound by writing: 32,768 x 1,600 in 31 us,
 // 105 MB written at 3.4 of the 4.0 TB/s that a memset reaches.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupArgs a)
 {
+    constexpr int kUnroll = kLookupUnroll<VEC>;
     pdl_entry();
-    const uint64_t i0 = (uint64_t)blockIdx.x * (kThreads * kLookupUnroll) + threadIdx.x;
-    uint4 w[kLookupUnroll];
+    const uint64_t i0 = (uint64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+    uint4 w[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kLookupUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
         const uint64_t i = i0 + u * kThreads;
         w[u] = make_uint4(0, 0, 0, 0);
         if (i < a.items) {
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_lookup(const LookupArgs a)
         }
     }
 #pragma unroll
-    for (int u = 0; u < kLookupUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
         const uint64_t i = i0 + u * kThreads;
         if (i < a.items) {
             const uint32_t t = (uint32_t)i / a.slots;
@@ -624,25 +628,59 @@ __device__ uint32_t lower_bound_warp(const uint2* pairs, uint32_t n, uint32_t ke
     return lo;
 }
 
+// Elements [c, c + 8) of the gradient's row, or zeros where not `there`, on their way
+// to registers: nothing looks at them before values() (which takes what load()
+// did).  VEC: the rows lie on 16-byte boundaries.
+template <bool VEC>
+struct Row8 {
+    Part8 part;
+
+    __device__ __forceinline__ void load(const uint16_t* row, uint64_t c, uint64_t dim, bool there)
+    {
+        part.load(row + c, there ? part_of8(c, dim) : 0);
+    }
+
+    __device__ __forceinline__ uint4 values(const uint16_t* row, uint64_t c, uint64_t dim, bool there) const
+    {
+        return part.values(row + c, there ? part_of8(c, dim) : 0);
+    }
+};
+
+template <>
+struct Row8<true> {
+    uint4 w;
+
+    __device__ __forceinline__ void load(const uint16_t* row, uint64_t c, uint64_t dim, bool there)
+    {
+        w = make_uint4(0, 0, 0, 0);
+        if (there)
+            w = load8<true>(row, c, dim);
+    }
+
+    __device__ __forceinline__ uint4 values(const uint16_t*, uint64_t, uint64_t, bool) const { return w; }
+};
+
 // Row v of the gradient at columns [c, c + 8): scale * acc, added onto `old`
 // (that row's values) if ADD.
 template <int DT, bool VEC, bool ADD>
 __device__ __forceinline__ void store_row(const GradArgs& a, uint32_t v, uint64_t c,
-                                          const float (&acc)[8], uint4 old)
+                                          const float (&acc)[8], const Row8<VEC>& old)
 {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         x[i] = acc[i] * a.scale;
+    uint16_t* row = a.d_table + (uint64_t)v * a.table_pitch;
     if (ADD)
-        add8<DT>(x, old);
-    store8_row<VEC>(a.d_table + (uint64_t)v * a.table_pitch, c, a.dim, narrow8<DT>(x));
+        add8<DT>(x, old.values(row, c, a.dim, true));
+    store8_row<VEC>(row, c, a.dim, narrow8<DT>(x));
 }
 
 template <bool VEC, bool ADD>
-__device__ __forceinline__ uint4 load_old(const GradArgs& a, uint32_t v, uint64_t c)
+__device__ __forceinline__ void load_old(const GradArgs& a, uint32_t v, uint64_t c, bool there, Row8<VEC>& old)
 {
-    return ADD ? load8<VEC>(a.d_table + (uint64_t)v * a.table_pitch, c, a.dim) : make_uint4(0, 0, 0, 0);
+    if (ADD)
+        old.load(a.d_table + (uint64_t)v * a.table_pitch, c, a.dim, there);
 }
 
 // Partial rows of a cell: [0] of a run that began before it and ends in it,
@@ -678,10 +716,11 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
         return;
     bool before = pair[-1].x == cur;   // the current run began before the cell
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    uint4 kept = make_uint4(0, 0, 0, 0);   // the table's row of the last run
+    Row8<VEC> kept;                        // the table's row of the last run
     const bool whole = c + 8 <= a.dim;     // not the ragged end of the rows
     for (int p = 0; p < kCell; p += BATCH) {
-        uint4 w[BATCH], old[BATCH];
+        uint4 w[BATCH];
+        Row8<VEC> old[BATCH];
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const uint2 at = pair[p + u];
@@ -690,8 +729,7 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
                 w[u] = load16_once(from + c, at.x < a.vocab && whole);
             else if (at.x < a.vocab)
                 w[u] = load8<true>(from, c, a.dim);
-            if (ADD && at.x < a.vocab && pair[p + u + 1].x != at.x)
-                old[u] = load_old<VEC, ADD>(a, at.x, c);
+            load_old<VEC, ADD>(a, at.x, c, at.x < a.vocab && pair[p + u + 1].x != at.x, old[u]);
         }
         if (LAYOUT != kFew && !whole)
 #pragma unroll
@@ -825,7 +863,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const GradArgs a)
         more[warp] = behind > kLongRun ? behind : 0;
     if (behind && behind <= kLongRun && slot < a.slots) {
         const uint32_t key = a.pairs[end - 1].x;
-        const uint4 old = load_old<VEC, ADD>(a, key, (uint64_t)slot * 8);
+        Row8<VEC> old;
+        load_old<VEC, ADD>(a, key, (uint64_t)slot * 8, true, old);
         float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 8
         for (uint32_t k = 0; k < behind; ++k)
@@ -859,8 +898,9 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const GradArgs a)
                 for (int i = 0; i < 8; ++i)
                     acc[i] += sums[k][lane][i];
             const uint32_t key = a.pairs[(first + r + 1) * kCell - 1].x;
-            store_row<DT, VEC, ADD>(a, key, (uint64_t)slot * 8, acc,
-                                    load_old<VEC, ADD>(a, key, (uint64_t)slot * 8));
+            Row8<VEC> old;
+            load_old<VEC, ADD>(a, key, (uint64_t)slot * 8, true, old);
+            store_row<DT, VEC, ADD>(a, key, (uint64_t)slot * 8, acc, old);
         }
         __syncthreads();
     }
@@ -1003,7 +1043,8 @@ extern "C" zero_status_t zero_embed_lookup(const zero_mat_t* table, const zero_i
     for (uint64_t t = 0; t < ids->count && e == cudaSuccess; t += step) {
         a.token0 = t;
         a.items = (ids->count - t < step ? ids->count - t : step) * a.slots;
-        const dim3 grid((unsigned)((a.items + kThreads * kLookupUnroll - 1) / (kThreads * kLookupUnroll)));
+        const uint32_t per_cta = kThreads * (vec ? kLookupUnroll<true> : kLookupUnroll<false>);
+        const dim3 grid((unsigned)((a.items + per_cta - 1) / per_cta));
         if (vec)
             e = launch_train(f16 ? k_embed_lookup<ZERO_F16, true> : k_embed_lookup<ZERO_BF16, true>,
                              grid, kThreads, 0, 1, stream, a);

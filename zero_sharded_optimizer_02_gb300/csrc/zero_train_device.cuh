@@ -102,6 +102,75 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8])
                       narrow2<DT>(v[6], v[7]));
 }
 
+// A word, a half or a byte, from global memory where `there` says so, else `other`.
+// Nothing here looks at it, as a select after the load would: the load stays in
+// flight until its value is needed.
+__device__ __forceinline__ uint32_t load_word(const void* p, bool there, uint32_t other)
+{
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+                 "@p ld.global.u32 %0, [%1];\n\t}"
+                 : "=&r"(w)
+                 : "l"(p), "r"((uint32_t)there), "r"(other));
+    return w;
+}
+
+__device__ __forceinline__ uint32_t load_half(const void* p, bool there, uint32_t other)
+{
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+                 "@p ld.global.u16 %0, [%1];\n\t}"
+                 : "=&r"(w)
+                 : "l"(p), "r"((uint32_t)there), "r"(other));
+    return w;
+}
+
+__device__ __forceinline__ uint32_t load_byte(const void* p, bool there, uint32_t other)
+{
+    uint32_t w;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+                 "@p ld.global.nc.u8 %0, [%1];\n\t}"
+                 : "=&r"(w)
+                 : "l"(p), "r"((uint32_t)there), "r"(other));
+    return w;
+}
+
+// Up to 8 elements of a row on their way to registers, where nothing looks at
+// them before values() does.  The row may start on any element: w[0..3] are the
+// aligned words that hold two of them, w[4] the one before those (at an odd
+// address) and w[5] the one behind; what is not there is zero.
+struct Part8 {
+    uint32_t w[6];
+
+    __device__ __forceinline__ void load(const uint16_t* p, uint32_t n)
+    {
+        const uint32_t odd = reinterpret_cast<uintptr_t>(p) / 2 % 2, head = odd & (n != 0), words = (n - head) / 2;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+            w[j] = load_word(p + head + 2 * j, j < words, 0);
+        w[4] = load_half(p, head, 0);
+        w[5] = load_half(p + n - 1, (n - head) % 2, 0);
+    }
+
+    // The elements in order, zeros behind them; p and n as load() had them.
+    __device__ __forceinline__ uint4 values(const uint16_t* p, uint32_t n) const
+    {
+        const uint32_t odd = reinterpret_cast<uintptr_t>(p) / 2 % 2, head = odd & (n != 0), words = (n - head) / 2;
+        uint32_t t[4];
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+            t[j] = j == words ? w[5] : w[j];
+        return make_uint4(__funnelshift_l(w[4] << 16, t[0], 16 * odd), __funnelshift_l(t[0], t[1], 16 * odd),
+                          __funnelshift_l(t[1], t[2], 16 * odd), __funnelshift_l(t[2], t[3], 16 * odd));
+    }
+};
+
+// The elements that [c, c + 8) has of a row of `cols`.
+__device__ __forceinline__ uint32_t part_of8(uint64_t c, uint64_t cols)
+{
+    return c >= cols ? 0 : cols - c < 8 ? (uint32_t)(cols - c) : 8;
+}
+
 // Elements [c, c + 8) of a row of `cols` elements; those past its end read as
 // zero and are not touched.  VEC: the row's elements c lie on 16-byte
 // boundaries (c is a multiple of 8).
@@ -110,12 +179,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, uint64_t c, uint64_t
 {
     if (VEC && c + 8 <= cols)
         return *reinterpret_cast<const uint4*>(row + c);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    Part8 part;
+    part.load(row + c, part_of8(c, cols));
+    return part.values(row + c, part_of8(c, cols));
 }
 
 template <bool VEC>
@@ -125,11 +191,21 @@ __device__ __forceinline__ void store8_row(uint16_t* row, uint64_t c, uint64_t c
         *reinterpret_cast<uint4*>(row + c) = v;
         return;
     }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // whole words where the row has them (Part8)
+    uint16_t* p = row + c;
+    const uint32_t n = part_of8(c, cols), odd = reinterpret_cast<uintptr_t>(p) / 2 % 2, head = odd & (n != 0);
+    const uint32_t words = (n - head) / 2;
+    const uint32_t t[4] = {__funnelshift_r(v.x, v.y, 16 * odd), __funnelshift_r(v.y, v.z, 16 * odd),
+                           __funnelshift_r(v.z, v.w, 16 * odd), v.w >> 16 * odd};
+    if (head)
+        p[0] = (uint16_t)v.x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            row[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    for (uint32_t j = 0; j < 4; ++j) {
+        if (j < words)
+            *reinterpret_cast<uint32_t*>(p + head + 2 * j) = t[j];
+        if (j == words && (n - head) % 2)
+            p[n - 1] = (uint16_t)t[j];
+    }
 }
 
 // Asynchronous copies of 16 or 8 bytes to shared memory, of which the first
@@ -146,19 +222,6 @@ __device__ __forceinline__ void cp_async8_part(void* dst, const void* src, uint3
                  : "memory");
 }
 
-// A word, or a byte, from global memory where `there` says so, else `other`.
-// Nothing here looks at it, as a select after the load would: the load stays in
-// flight until its value is needed.
-__device__ __forceinline__ uint32_t load_word(const void* p, bool there, uint32_t other)
-{
-    uint32_t w;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
-                 "@p ld.global.nc.u32 %0, [%1];\n\t}"
-                 : "=&r"(w)
-                 : "l"(p), "r"((uint32_t)there), "r"(other));
-    return w;
-}
-
 // 16 bytes that are read once (not kept in L1), or zeros.
 __device__ __forceinline__ uint4 load16_once(const void* p, bool there)
 {
@@ -169,16 +232,6 @@ __device__ __forceinline__ uint4 load16_once(const void* p, bool there)
                  : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
                  : "l"(p), "r"((uint32_t)there));
     return r;
-}
-
-__device__ __forceinline__ uint32_t load_byte(const void* p, bool there, uint32_t other)
-{
-    uint32_t w;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
-                 "@p ld.global.nc.u8 %0, [%1];\n\t}"
-                 : "=&r"(w)
-                 : "l"(p), "r"((uint32_t)there), "r"(other));
-    return w;
 }
 
 // -- the 8-bit checkpoint -------------------------------------------------------
