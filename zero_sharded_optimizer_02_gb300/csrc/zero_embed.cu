@@ -653,7 +653,7 @@ struct Row8<true> {
     __device__ __forceinline__ void load(const uint16_t* row, uint64_t c, uint64_t dim, bool there)
     {
         w = make_uint4(0, 0, 0, 0);
-        if (there)
+        if (there)   // predicated loads here spill: 65,536 x 1,600 added in 106 us, so 101
             w = load8<true>(row, c, dim);
     }
 
@@ -725,17 +725,18 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
         for (int u = 0; u < BATCH; ++u) {
             const uint2 at = pair[p + u];
             const uint16_t* from = a.d_out + (uint64_t)at.y * a.d_out_pitch;
-            if (LAYOUT != kFew)
-                w[u] = load16_once(from + c, at.x < a.vocab && whole);
-            else if (at.x < a.vocab)
-                w[u] = load8<true>(from, c, a.dim);
+            w[u] = load16<LAYOUT != kFew>(from + c, at.x < a.vocab && whole);
             load_old<VEC, ADD>(a, at.x, c, at.x < a.vocab && pair[p + u + 1].x != at.x, old[u]);
         }
-        if (LAYOUT != kFew && !whole)
+        if (!whole) {
+            const uint32_t n = part_of8(c, a.dim);
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
-                if (pair[p + u].x < a.vocab)
-                    w[u] = load8<true>(a.d_out + (uint64_t)pair[p + u].y * a.d_out_pitch, c, a.dim);
+                w[u] = load_tail8(a.d_out + (uint64_t)pair[p + u].y * a.d_out_pitch + c, pair[p + u].x < a.vocab ? n : 0);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                w[u] = tail8(w[u], n);
+        }
 #pragma unroll
         for (int u = 0; u < BATCH; ++u) {
             const uint32_t key = pair[p + u].x;

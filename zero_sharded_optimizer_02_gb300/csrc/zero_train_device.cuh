@@ -222,16 +222,42 @@ __device__ __forceinline__ void cp_async8_part(void* dst, const void* src, uint3
                  : "memory");
 }
 
-// 16 bytes that are read once (not kept in L1), or zeros.
-__device__ __forceinline__ uint4 load16_once(const void* p, bool there)
+// 16 bytes from global memory, or zeros.  ONCE: not kept in L1.
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16(const void* p, bool there)
 {
     uint4 r;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
-                 "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                 : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
-                 : "l"(p), "r"((uint32_t)there));
+    if (ONCE)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+                     "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                     "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+                     : "l"(p), "r"((uint32_t)there));
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+                     "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                     "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+                     : "l"(p), "r"((uint32_t)there));
     return r;
+}
+
+// The n < 8 elements of a row's ragged end, at a 16-byte boundary: four of them
+// in x and y, two in z, one in w, as n has them, for tail8() to put in order.
+__device__ __forceinline__ uint4 load_tail8(const uint16_t* p, uint32_t n)
+{
+    uint4 r;
+    r.x = load_word(p, n & 4, 0);
+    r.y = load_word(p + 2, n & 4, 0);
+    r.z = load_word(p + (n & 4), n & 2, 0);
+    r.w = load_half(p + (n & 6), n & 1, 0);
+    return r;
+}
+
+__device__ __forceinline__ uint4 tail8(uint4 r, uint32_t n)
+{
+    const uint32_t first = n & 2 ? r.z : r.w, second = n & 2 ? r.w : 0;
+    return n & 4 ? make_uint4(r.x, r.y, first, second) : make_uint4(first, second, 0, 0);
 }
 
 // -- the 8-bit checkpoint -------------------------------------------------------
