@@ -385,6 +385,18 @@ def test_embed_grad_many_tokens(tokens, vocab):
     check_embed_grad(act(g, tokens, 40, "bf16", 0.1), ids, 40.0, False, vocab, "bf16")
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(16000, 700, 801), (13001, 20000, 1607), (21011, 1200, 45), (20001, 333, 130),
+                                              (70, 90, 1), (33, 2000, 7), (2049, 5, 9)])
+@pytest.mark.parametrize("add,offset,pad", [(False, 0, 0), (False, 1, 0), (False, 7, 3), (True, 2, 0), (True, 5, 0), (True, 0, 7)])
+def test_embed_grad_rows_anywhere(tokens, vocab, dim, add, offset, pad):
+    """Table rows that start on any element, with ends of every length, in short and long batches."""
+    g = gen(tokens + dim + offset)
+    u = torch.rand(tokens, generator=g, device=DEV, dtype=torch.float64)
+    ids = torch.exp(u * torch.log(torch.tensor(float(vocab)))).long().clamp(1, vocab) - 1
+    ids[::11] = -1
+    check_embed_grad(act(g, tokens, dim, "bf16", 0.1), ids, 0.5, add, vocab, "bf16", offset, pitch=dim + pad, seed=dim)
+
+
 def test_embed_grad_ids_outside_the_table():
     g = gen(2)
     d_out, table = act(g, 100, 16, "f16"), table_of(g, 10, 16, "f16")

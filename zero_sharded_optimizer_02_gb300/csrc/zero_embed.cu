@@ -581,10 +581,10 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 //   kMany  over kManyTokens tokens: cells of 32 too.
 // Smaller cells are more threads and shorter chains of loads, but leave more
 // partial rows to write and join.  As few, some and many, us, added:
-//   1,021 x 768    11, 13, 17       16,384 x 768    30, 26, 29
-//   20,000 x 256   27, 29, 32       20,000 x 1,600  61, 57, 57 (stored)
-//   24,000 x 1,600 61, 56, 53       65,536 x 768    87, 71, 66
-//   65,536 x 256   48, 49, 45       65,536 x 1,600  139, 119, 106
+//   1,021 x 768    11, 12, 16       16,384 x 768    29, 24, 27
+//   20,000 x 256   27, 28, 31       20,000 x 1,600  59, 54, 55 (stored)
+//   24,000 x 1,600 60, 54, 50       65,536 x 768    76, 68, 61
+//   65,536 x 256   47, 46, 43       65,536 x 1,600  134, 112, 101
 // Only long batches of narrow rows lose: 24,000 x 256 28, 30, 32.
 enum Layout { kFew, kSome, kMany };
 template <int LAYOUT>
