@@ -708,17 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 } else if (i < a.ins) {
                     uint16_t* p = a.dw + (o0 + c) * a.dw_pitch + i;
                     const uint32_t n = o0 + c < a.outs ? (uint32_t)min((uint64_t)32, a.outs - o0 - c) : 0;
+                    // rows of dw that start anywhere: all old values in flight at once.  425
+                    // tokens, 3,742 -> 2,688 added in 48 us; 16 at a time 55, 8 68, 1 129.
+                    uint32_t old[32];
 #pragma unroll
-                    for (int h = 0; h < 32; h += 8) {
-                        float old[8];
+                    for (int j = 0; j < 32; ++j)
+                        old[j] = load_half(p + j * a.dw_pitch, a.add && j < n, 0);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            old[j] = a.add && h + j < n ? widen1<DT>(p[(h + j) * a.dw_pitch]) : 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (h + j < n)
-                                p[(h + j) * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[h + j]) * gain + old[j]);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (j < n)
+                            p[j * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[j]) * gain + widen1<DT>((uint16_t)old[j]));
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
