@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 // Vectors of a lookup's thread.  32,768 x 1,600 in 31 us with 2, 34 with 1, 32 with
-// 4; of a table whose rows start on any element 39, 37 and 43.
+// 4; of a table whose rows start on any element in 39 with 2, 37 with 1.
 template <bool VEC>
 constexpr int kLookupUnroll = VEC ? 2 : 1;
 
@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(kThreads) k_sort_move(const SortArgs a)
 // holds it, or in the last pass to global memory.  The multi-launch passes
 // take about 6 us for each of their launches.
 // 65,536 tokens of 50,257 numbers (two passes of 8 bits): 25 us, of which the
-// scattered stores to the other CTAs take 5, ranking 8; 1,021 tokens (one CTA): 7 us.
+// scattered stores to the other CTAs take 5, ranking 8.  Clusters of 16 CTAs, which
+// not every part of a GPU can hold, took 5 us less there (1 more up to 16,384
+// tokens), and nothing less where the rows of absent tokens are written beside it.
 constexpr int kClusterCtas = 8;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
@@ -653,7 +655,7 @@ struct Row8<true> {
     __device__ __forceinline__ void load(const uint16_t* row, uint64_t c, uint64_t dim, bool there)
     {
         w = make_uint4(0, 0, 0, 0);
-        if (there)   // predicated loads here spill: 65,536 x 1,600 added in 106 us, so 101
+        if (there)   // predicated loads would spill: 65,536 x 1,600 added in 106 us, not 101
             w = load8<true>(row, c, dim);
     }
 
@@ -732,7 +734,8 @@ __device__ __forceinline__ void sum_cell(const GradArgs& a, const uint2* pair, u
             const uint32_t n = part_of8(c, a.dim);
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
-                w[u] = load_tail8(a.d_out + (uint64_t)pair[p + u].y * a.d_out_pitch + c, pair[p + u].x < a.vocab ? n : 0);
+                w[u] = load_tail8(a.d_out + (uint64_t)pair[p + u].y * a.d_out_pitch + c,
+                                  pair[p + u].x < a.vocab ? n : 0);
 #pragma unroll
             for (int u = 0; u < BATCH; ++u)
                 w[u] = tail8(w[u], n);
@@ -1130,9 +1133,9 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
         c.passes = (bits + kClusterDigitBits - 1) / kClusterDigitBits;
         c.bits = (bits + c.passes - 1) / c.passes;
         const uint32_t items = (n + kClusterCtas * kClusterThreads - 1) / (kClusterCtas * kClusterThreads);
+        const uint32_t count_ctas = (n + kWarps - 1) / kWarps < kCountCtas ? (n + kWarps - 1) / kWarps : kCountCtas;
         e = n <= kCountTokens
-                ? launch_train(k_sort_count_all, dim3((n + kWarps - 1) / kWarps < kCountCtas ? (n + kWarps - 1) / kWarps : kCountCtas),
-                               kThreads, 0, 1, stream, c)
+                ? launch_train(k_sort_count_all, dim3(count_ctas), kThreads, 0, 1, stream, c)
             : items <= 1 ? launch_cluster_sort<1>(c, stream)
             : items <= 2 ? launch_cluster_sort<2>(c, stream)
             : items <= 4 ? launch_cluster_sort<4>(c, stream)
@@ -1188,7 +1191,8 @@ extern "C" zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids
     a.per_cta = g.per_cta;
     a.cell_ctas = (a.cells + a.per_cta - 1) / a.per_cta;
     a.scale = scale;
-    const uint32_t zero_ctas = accumulate || (n && n <= kClusterTokens) ? 0 : (uint32_t)(((uint64_t)vocab + kZeroRows - 1) / kZeroRows);
+    const uint32_t zero_ctas =
+        accumulate || (n && n <= kClusterTokens) ? 0 : (uint32_t)(((uint64_t)vocab + kZeroRows - 1) / kZeroRows);
     const bool add = accumulate != 0;
     e = d_table->dtype == ZERO_F16 ? launch_sums<ZERO_F16>(a, zero_ctas, vec, add, g.layout, stream)
                                    : launch_sums<ZERO_BF16>(a, zero_ctas, vec, add, g.layout, stream);

@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (j < n)
-                            p[j * a.dw_pitch] = narrow1<DT>(__uint_as_float(v[j]) * gain + widen1<DT>((uint16_t)old[j]));
+                            p[j * a.dw_pitch] =
+                                narrow1<DT>(__uint_as_float(v[j]) * gain + widen1<DT>((uint16_t)old[j]));
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
