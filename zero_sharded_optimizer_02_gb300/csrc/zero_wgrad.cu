@@ -47,8 +47,9 @@ constexpr int kGroupBytes = 64 * kStepT * 2;                 // 64 elements of e
 constexpr int kRawBytes = kHalf * kStepT;                    // 8 KB
 constexpr int kScaleBytes = kStepT * 16;                     // the steps of 4 blocks of every token
 constexpr int kEpilogueWarps = 4;
-constexpr int kTurnPitch = 32 * 2 + 16;                      // bytes of a row of a turned 32 x 32 tile
-constexpr int kTurnBytes = 32 * kTurnPitch;
+constexpr int kTurnRows = 16;                                // outputs of a tile that is turned
+constexpr int kTurnPitch = 32 * 2 + 16;                      // bytes of an output's 32 inputs there
+constexpr int kTurnBytes = 2 * kTurnRows * kTurnPitch;       // two tiles
 constexpr int kYAt = kStages * kOperandBytes;
 constexpr int kRawAt = kYAt + kStages * kOperandBytes;
 constexpr int kScaleAt = kRawAt + kRawStages * kRawBytes;
@@ -361,6 +362,16 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ uint32_t load_shared_half(uint32_t addr, bool there)
+{
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0;\n\t"
+                 "@p ld.shared.u16 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "r"(addr), "r"((uint32_t)there));
+    return v;
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_weight_grad(const __grid_constant__ CUtensorMap dy, const __grid_constant__ CUtensorMap q,
@@ -649,18 +660,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // epilogue: warp w of the CTA may read the tensor memory lanes 32 (w mod 4) .. + 31;
         // a lane is an input, a column an output
         const uint32_t quarter = warp % 4;
-        // A tile of 32 inputs x 32 outputs is turned in shared memory, so that a
-        // row of dw is stored 64 bytes at a time by four lanes.
+        // A tile of 32 inputs x kTurnRows outputs is turned in shared memory, so that a
+        // row of dw is stored 64 bytes at a time by four lanes.  What it is added to is
+        // copied there a tile ahead, the first before the products are done: 1,024 tokens,
+        // 4,096 -> 4,096 added in 56 us, 69 where it was loaded when needed.
         const uint32_t turn = base + kTurnAt + quarter * kTurnBytes;
-        const uint32_t mine = turn + lane * 2, line = turn + lane / 4 * kTurnPitch + lane % 4 * 16;
+        const uint32_t mine = lane * 2, line = lane / 4 * kTurnPitch + lane % 4 * 16;
+        constexpr int kOld = 16, kTurnOld = 8;
         uint32_t buf = 0, buf_phase = 0;
         for (uint32_t u = pair; u < a.plan.units; u += pairs) {
             const Unit t = unit_at(a.plan, u);
+            const uint32_t r = rank * kHalf + quarter * 32 + lane;
+            const uint64_t o0 = (uint64_t)t.to * kTileO;
+            const uint32_t outs = o0 < a.outs ? (uint32_t)min((uint64_t)kTileO, a.outs - o0) : 0;
+            const uint32_t i = t.ti * kTileI + r;
+            uint16_t* dw = a.dw + o0 * a.dw_pitch + (i - lane);   // the warp's corner of the tile
+            const bool turned = t.part < 0 && a.dw_vec && (uint64_t)i - lane + 32 <= a.ins;
+            const auto fetch_old = [&](uint32_t c) {   // of the tile of outputs c ..
+                if (turned && a.add && c < kTileO)
+#pragma unroll
+                    for (int j = 0; j < kTurnRows; j += 8) {
+                        const uint32_t to = turn + c / kTurnRows % 2 * (kTurnBytes / 2) + line + j * kTurnPitch;
+                        const uint32_t o = c + j + lane / 4;
+                        cp_async16_part(reinterpret_cast<void*>(__cvta_shared_to_generic(to)),
+                                        dw + o * a.dw_pitch + lane % 4 * 8, o < outs ? 16 : 0);
+                    }
+                cp_async_commit();
+            };
+            fetch_old(0);
             const bool ok = __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t r = rank * kHalf + quarter * 32 + lane;
-            const uint64_t i = (uint64_t)t.ti * kTileI + r;
-            const uint64_t o0 = (uint64_t)t.to * kTileO;
             const float gain = a.gain && i < a.ins ? widen1<DT>(a.gain[i]) : 1.0f;
             for (uint32_t c = 0; c < kTileO; c += 32) {
                 uint32_t v[32];
@@ -674,51 +703,51 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         p[(uint32_t)j * kTileI] = __uint_as_float(v[j]);
-                } else if (a.dw_vec && i - lane + 32 <= a.ins) {
-                    uint16_t* p = a.dw + (o0 + c + lane / 4) * a.dw_pitch + (i - lane) + lane % 4 * 8;
-                    __syncwarp();   // the previous tile has been read
-                    if (a.add) {
-                        uint4 w[4];
+                } else if (turned) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (o0 + c + j * 8 + lane / 4 < a.outs)
-                                w[j] = *reinterpret_cast<const uint4*>(p + j * 8 * a.dw_pitch);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            store_shared16(line + j * 8 * kTurnPitch, w[j]);
+                    for (int h = 0; h < 32; h += kTurnRows) {
+                        fetch_old(c + h + kTurnRows);
+                        cp_async_wait<1>();
                         __syncwarp();
-                    }
+                        const uint32_t tile = turn + h / kTurnRows % 2 * (kTurnBytes / 2);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float x = __uint_as_float(v[j]) * gain;
-                        if (a.add) {
-                            uint16_t b;
-                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(mine + j * kTurnPitch));
-                            x += widen1<DT>(b);
+                        for (int j = 0; j < kTurnRows; j += kTurnOld) {
+                            uint32_t old[kTurnOld];
+#pragma unroll
+                            for (int k = 0; k < kTurnOld; ++k)
+                                old[k] = load_shared_half(tile + mine + (j + k) * kTurnPitch, a.add);
+#pragma unroll
+                            for (int k = 0; k < kTurnOld; ++k)
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + mine + (j + k) * kTurnPitch),
+                                             "h"(narrow1<DT>(__uint_as_float(v[h + j + k]) * gain +
+                                                             widen1<DT>((uint16_t)old[k])))
+                                             : "memory");
                         }
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(mine + j * kTurnPitch), "h"(narrow1<DT>(x))
-                                     : "memory");
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < kTurnRows; j += 8)
+                            if (c + h + j + lane / 4 < outs)
+                                *reinterpret_cast<uint4*>(dw + (c + h + j + lane / 4) * a.dw_pitch + lane % 4 * 8) =
+                                    load_shared16(tile + line + j * kTurnPitch);
+                        __syncwarp();   // the tile has been read
                     }
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (o0 + c + j * 8 + lane / 4 < a.outs)
-                            *reinterpret_cast<uint4*>(p + j * 8 * a.dw_pitch) =
-                                load_shared16(line + j * 8 * kTurnPitch);
                 } else if (i < a.ins) {
-                    uint16_t* p = a.dw + (o0 + c) * a.dw_pitch + i;
-                    const uint32_t n = o0 + c < a.outs ? (uint32_t)min((uint64_t)32, a.outs - o0 - c) : 0;
-                    // rows of dw that start anywhere: all old values in flight at once.  425
-                    // tokens, 3,742 -> 2,688 added in 48 us; 16 at a time 55, 8 68, 1 129.
-                    uint32_t old[32];
+                    uint16_t* p = dw + c * a.dw_pitch + lane;
+                    const uint32_t n = outs > c ? min(32u, outs - c) : 0;
+                    // rows of dw that start anywhere: kOld old values in flight.  425 tokens,
+                    // 3,742 -> 2,688 added in 40 us; with 8 53, with 32, which spill, 79.
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        old[j] = load_half(p + j * a.dw_pitch, a.add && j < n, 0);
+                    for (int h = 0; h < 32; h += kOld) {
+                        uint32_t old[kOld];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n)
-                            p[j * a.dw_pitch] =
-                                narrow1<DT>(__uint_as_float(v[j]) * gain + widen1<DT>((uint16_t)old[j]));
+                        for (int j = 0; j < kOld; ++j)
+                            old[j] = load_half(p + (h + j) * a.dw_pitch, a.add && h + j < n, 0);
+#pragma unroll
+                        for (int j = 0; j < kOld; ++j)
+                            if (h + j < n)
+                                p[(h + j) * a.dw_pitch] =
+                                    narrow1<DT>(__uint_as_float(v[h + j]) * gain + widen1<DT>((uint16_t)old[j]));
+                    }
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
