@@ -481,8 +481,9 @@ def test_weight_grad_larger(tokens, outs, ins, pitch):
     check_weight_grad(tokens, outs, ins, "f16", False, True, pitch=pitch)
 
 
-@pytest.mark.parametrize("tokens,outs,ins,pitch,offset", [(70, 5001, 2100, 2104, 0), (5, 4096, 2560, 2560, 8), (130, 2600, 2056, 2056, 0),
-                                                          (1030, 4343, 2071, 2080, 16), (1, 9000, 544, 544, 2)])
+@pytest.mark.parametrize("tokens,outs,ins,pitch,offset", [
+    (70, 5001, 2100, 2104, 0), (5, 4096, 2560, 2560, 8), (130, 2600, 2056, 2056, 0), (1030, 4343, 2071, 2080, 16),
+    (1, 9000, 544, 544, 2)])
 @pytest.mark.parametrize("add", [False, True])
 def test_weight_grad_more_tiles_than_pairs(tokens, outs, ins, pitch, offset, add):
     """A pair of CTAs takes several tiles, and writes one while it multiplies the next."""

@@ -19,7 +19,7 @@
 // Tiles that would leave pairs idle in the last wave are cut along the tokens
 // into `splits` parts each, whose fp32 sums a second launch adds in order.
 //
-// 16,384 tokens, 4,096 -> 16,384: 1.46 ms, 1.51 PFLOP/s; bound by the
+// 16,384 tokens, 4,096 -> 16,384: 1.46 to 1.51 ms, 1.48 PFLOP/s; bound by the
 // shared-memory pipe (92% busy), which carries the operands to the tensor cores,
 // the bytes to the converting warps and their values back.
 //
