@@ -222,12 +222,12 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// Waits for the phase of parity `parity`; false if that took over kWaitNs or
+// Waits for the phase of parity `parity`; false if that took over limit_ns or
 // another wait of this CTA has run out (`failed`, shared memory).  Waits that
 // poll slow down each other and every arrival, and two dozen warps wait in this
 // kernel: those whose answer is not urgent sleep NS nanoseconds between tries.
 template <int NS>
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* failed)
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* failed, uint64_t limit_ns)
 {
     uint64_t t0 = 0;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
@@ -239,7 +239,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
             const uint64_t t = global_ns();
             if (!t0)
                 t0 = t;
-            if (*failed || t - t0 > kWaitNs)
+            if (*failed || t - t0 > limit_ns)
                 break;
         }
     }
@@ -247,6 +247,21 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return false;
 }
 constexpr int kNow = 0, kSoon = 64, kLater = 500;   // how long a wait sleeps between tries
+
+// Before a CTA ends: waits until the copies last issued for each of the `armed`
+// stages have landed.  After a wait has run out these barriers may never
+// complete (they count conversions too), so one limit holds for all of them: a
+// copy takes microseconds.
+constexpr uint64_t kDrainNs = 1000 * 1000 * 1000;
+__device__ __forceinline__ void drain_copies(uint32_t bars, uint32_t stages, uint32_t armed, uint32_t phases)
+{
+    const uint64_t t0 = global_ns();
+    for (uint32_t s = 0; s < stages; ++s)
+        if (armed >> s & 1)
+            for (uint32_t i = 0; i < (1u << 30) && !mbar_try_wait(bars + 8 * s, phases >> s & 1); ++i)
+                if (global_ns() - t0 > kDrainNs)
+                    return;
+}
 
 // A box of a matrix into this CTA's shared memory at dst; its bytes count on
 // this CTA's barrier `bar`.
@@ -328,6 +343,7 @@ struct WgradArgs {
     uint64_t tokens, outs, ins;
     uint32_t add;
     uint32_t dw_vec;     // dw's rows start on 16-byte boundaries
+    uint64_t wait_ns;    // longest wait
     Plan plan;
 };
 
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Unit t = unit_at(a.plan, u);
                 const int x = (int)(t.to * kTileO + rank * kHalf);
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    if (!wait_phase<kSoon>(empty + 8 * stage, phase ^ 1, failed)) {
+                    if (!wait_phase<kSoon>(empty + 8 * stage, phase ^ 1, failed, a.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -456,9 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // The pair does not end under its own copies: both CTAs' bytes count on
             // the first one's barriers, and the other waits for it below.
             if (rank == 0)
-                for (uint32_t s = 0; s < kStages; ++s)
-                    if (armed >> s & 1)
-                        mbar_wait(full + 8 * s, armed_phase >> s & 1, kWaitNs);
+                drain_copies(full, kStages, armed, armed_phase);
         }
     } else if (seat.role == kRoleProducts) {
         if (lane == 0 && rank == 0) {   // products
@@ -466,13 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool ok = true;
             for (uint32_t u = pair; u < a.plan.units && ok; u += pairs) {
                 const Unit t = unit_at(a.plan, u);
-                ok = wait_phase<kNow>(tmem_empty + 8 * buf, buf_phase ^ 1, failed);
+                ok = wait_phase<kNow>(tmem_empty + 8 * buf, buf_phase ^ 1, failed, a.wait_ns);
                 if (!ok)
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t acc = tmem + buf * kTileO;
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    ok = wait_phase<kNow>(full + 8 * stage, phase, failed);
+                    ok = wait_phase<kNow>(full + 8 * stage, phase, failed, a.wait_ns);
                     if (!ok)
                         break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -512,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         static_assert(kGroups <= kStages && kGroups <= kRawStages, "a group's first stage");
         for (uint32_t n = group; n < total; n += kGroups) {
             // one warp of the group waits, the others for it
-            if (leads && !(wait_phase<kNow>(raw_full + 8 * rstage, rphase, failed) &&
-                           wait_phase<kNow>(empty + 8 * stage, phase ^ 1, failed)))
+            if (leads && !(wait_phase<kNow>(raw_full + 8 * rstage, rphase, failed, a.wait_ns) &&
+                           wait_phase<kNow>(empty + 8 * stage, phase ^ 1, failed, a.wait_ns)))
                 *stopped = 1;
             asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * kGroupWarps) : "memory");
             if (*stopped)
@@ -560,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Unit t = unit_at(a.plan, u);
                 const int x = (int)(t.ti * kTileI + rank * kHalf);
                 for (uint32_t k = t.k0; k < t.k1; ++k) {
-                    ok = wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed);
+                    ok = wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed, a.wait_ns);
                     if (!ok)
                         break;
                     mbar_arrive_expect_tx(raw_full + 8 * stage, kRawBytes);
@@ -574,9 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                 }
             }
-            for (uint32_t s = 0; s < kRawStages; ++s)   // as for dy's
-                if (armed >> s & 1)
-                    mbar_wait(raw_full + 8 * s, armed_phase >> s & 1, kWaitNs);
+            drain_copies(raw_full, kRawStages, armed, armed_phase);   // as for dy's
         }
     } else if (seat.role == kRoleScales) {
         // scale bytes: pair g of the warps takes steps g, g + kTurns, ...; lane l of
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t n = n0 + i * kTurns;
                 if (n >= total || !ok)
                     break;
-                ok = __all_sync(0xFFFFFFFFu, wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed));
+                ok = __all_sync(0xFFFFFFFFu, wait_phase<kSoon>(raw_empty + 8 * stage, phase ^ 1, failed, a.wait_ns));
                 if (!ok)
                     break;
                 const uint32_t w = __funnelshift_r(w0[i], w1[i], shift);
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 cp_async_commit();
             };
             fetch_old(0);
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed));
+            const bool ok = __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed, a.wait_ns));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const float gain = a.gain && i < a.ins ? widen1<DT>(a.gain[i]) : 1.0f;
             for (uint32_t c = 0; c < kTileO; c += 32) {
@@ -832,29 +844,62 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// Map of a matrix for boxes of kStepT rows x `box` columns (128 bytes wide) in
+// Map of a matrix for boxes of box_rows x `box` columns (128 bytes wide) in
 // the 128-byte swizzle; what lies outside the matrix reads as zero.
 bool encode_rows(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, void* base, uint64_t cols,
-                 uint64_t rows, uint64_t pitch_bytes, uint32_t box)
+                 uint64_t rows, uint64_t pitch_bytes, uint32_t box, uint32_t box_rows)
 {
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {pitch_bytes};
-    const cuuint32_t boxes[2] = {box, kStepT}, unit[2] = {1, 1};
+    const cuuint32_t boxes[2] = {box, box_rows}, unit[2] = {1, 1};
     return encode(map, type, 2, base, dims, strides, boxes, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The maps of dy and of the checkpoint's bytes, for boxes of so many tokens.
+bool encode_operands(EncodeTiled encode, CUtensorMap* ymap, CUtensorMap* qmap, const zero_mat_t* dy, const zero_act8_t* x,
+                     uint32_t y_tokens = kStepT, uint32_t q_tokens = kStepT)
+{
+    return encode_rows(encode, ymap,
+                       dy->dtype == ZERO_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       dy->base, dy->cols, dy->rows, 2 * dy->pitch, 64, y_tokens) &&
+           encode_rows(encode, qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->q, x->cols, x->rows, x->q_pitch, kHalf, q_tokens);
+}
+
+WgradArgs make_args(const zero_act8_t* x, const void* gain, uint32_t accumulate, const zero_mat_t* dw, void* workspace,
+                    const Plan& plan)
+{
+    WgradArgs a = {};
+    a.q = x->q;
+    a.scale = x->scale;
+    a.gain = static_cast<const uint16_t*>(gain);
+    a.dw = static_cast<uint16_t*>(dw->base);
+    a.parts = static_cast<float*>(workspace);
+    a.q_pitch = x->q_pitch;
+    a.scale_pitch = x->scale_pitch;
+    a.dw_pitch = dw->pitch;
+    a.tokens = x->rows;
+    a.outs = dw->rows;
+    a.ins = dw->cols;
+    a.add = accumulate;
+    a.dw_vec = (uintptr_t)dw->base % 16 == 0 && dw->pitch % 8 == 0;
+    a.wait_ns = kWaitNs;
+    a.plan = plan;
+    return a;
+}
+
 template <int DT>
-cudaError_t launch_products(const CUtensorMap& dy, const CUtensorMap& q, const WgradArgs& a, bool vec, void* stream)
+cudaError_t launch_products(const CUtensorMap& dy, const CUtensorMap& q, const WgradArgs& a, void* stream,
+                            uint32_t max_pairs = kPairs)
 {
     static std::atomic<uint64_t> allowed{0};
     allow_smem(k_weight_grad<DT>, kSmemBytes, allowed);
-    const uint32_t pairs = a.plan.units < kPairs ? a.plan.units : kPairs;
+    const uint32_t pairs = a.plan.units < max_pairs ? a.plan.units : max_pairs;
     cudaError_t e = launch_train(k_weight_grad<DT>, dim3(2 * pairs), kThreads, kSmemBytes, 1, stream, dy, q, a);
     if (e == cudaSuccess && a.plan.splits > 1) {
         const uint32_t cut = a.plan.tiles_i * a.plan.tiles_o - a.plan.full;
-        e = launch_train(vec ? k_weight_join<DT, true> : k_weight_join<DT, false>, dim3(cut * kJoinCtas),
+        e = launch_train(a.dw_vec ? k_weight_join<DT, true> : k_weight_join<DT, false>, dim3(cut * kJoinCtas),
                          kJoinThreads, 0, 1, stream, a);
     }
     return e;
@@ -917,34 +962,16 @@ extern "C" zero_status_t zero_act_weight_grad(const zero_mat_t* dy, const zero_a
     if (st != ZERO_OK)
         return st;
 
-    WgradArgs a = {};
-    a.q = x->q;
-    a.scale = x->scale;
-    a.gain = static_cast<const uint16_t*>(gain);
-    a.dw = static_cast<uint16_t*>(dw->base);
-    a.parts = static_cast<float*>(workspace);
-    a.q_pitch = x->q_pitch;
-    a.scale_pitch = x->scale_pitch;
-    a.dw_pitch = dw->pitch;
-    a.tokens = dy->rows;
-    a.outs = dw->rows;
-    a.ins = dw->cols;
-    a.add = accumulate;
-    a.plan = plan;
+    const WgradArgs a = make_args(x, gain, accumulate, dw, workspace, plan);
     if (!some)
         return train_status(launch_train(k_weight_zero, dim3((unsigned)((a.ins + 255) / 256),
                                          (unsigned)(a.outs < 1024 ? a.outs : 1024)), 256, 0, 1, stream, a));
     const EncodeTiled encode = encode_tiled();
     if (!encode)
         return ZERO_ERR_CUDA;
-    const bool f16 = dy->dtype == ZERO_F16;
     CUtensorMap ymap, qmap;
-    if (!encode_rows(encode, &ymap, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     dy->base, dy->cols, dy->rows, 2 * dy->pitch, 64) ||
-        !encode_rows(encode, &qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->q, x->cols, x->rows, x->q_pitch, kHalf))
+    if (!encode_operands(encode, &ymap, &qmap, dy, x))
         return ZERO_ERR_CUDA;
-    const bool vec = (uintptr_t)dw->base % 16 == 0 && dw->pitch % 8 == 0;
-    a.dw_vec = vec;
-    return train_status(f16 ? launch_products<ZERO_F16>(ymap, qmap, a, vec, stream)
-                            : launch_products<ZERO_BF16>(ymap, qmap, a, vec, stream));
+    return train_status(dy->dtype == ZERO_F16 ? launch_products<ZERO_F16>(ymap, qmap, a, stream)
+                                              : launch_products<ZERO_BF16>(ymap, qmap, a, stream));
 }
