@@ -3,8 +3,9 @@
 Its waits are on its own copies and products, which always arrive, so the
 kernel is launched here with arguments of the test's (tests/c/wgrad_waits.cu):
 copies of half a step's tokens, whose missing bytes nothing brings, with a wait
-of 20 ms.  Every access stays inside its buffers, every wait ends, and the CUDA
-context stays usable."""
+of 20 ms; or whole copies with a wait far shorter than a tile takes.  Every
+access stays inside its buffers, every wait ends, and the CUDA context stays
+usable."""
 import ctypes as C
 import os
 import subprocess
@@ -76,3 +77,17 @@ def test_a_wait_that_runs_out_ends_the_call_soon(run, short):
     assert time.monotonic() - t0 < 3.0
     assert bool(torch.isnan(dw).all())
     assert torch.equal(right(dy, q, s, False, dw), want)   # an ordinary call afterwards
+
+
+def test_a_wait_that_runs_out_under_products(run):
+    """Nothing is missing, but the epilogue's waits, which look at the clock every 64 tries,
+    run out on tiles of 16,000 steps (5 ms), while products are issued.  The call ends, and
+    an undisturbed one behind it gives what it gave before."""
+    dy, q, s = problem(1_024_000, 1024, 512, "bf16")
+    old = torch.randn(1024, 512, generator=gen(1), device=DEV).bfloat16()
+    whole = run(dy, q, s, True, old.clone(), 10 ** 9, one_pair=True)
+    assert bool(torch.isfinite(whole).all())
+    for wait_ns in (0, 100_000):
+        lost = run(dy, q, s, True, old.clone(), wait_ns, one_pair=True)
+        assert bool(torch.isnan(lost).any())
+        assert torch.equal(run(dy, q, s, True, old.clone(), 10 ** 9, one_pair=True), whole)

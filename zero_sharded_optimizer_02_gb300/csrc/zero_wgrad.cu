@@ -55,7 +55,7 @@ constexpr int kRawAt = kYAt + kStages * kOperandBytes;
 constexpr int kScaleAt = kRawAt + kRawStages * kRawBytes;
 constexpr int kTurnAt = kScaleAt + kRawStages * kScaleBytes;
 constexpr int kBarrierAt = kTurnAt + kEpilogueWarps * kTurnBytes;
-constexpr int kBarriers = 2 * kStages + 2 * kRawStages + 4;
+constexpr int kBarriers = 2 * kStages + 2 * kRawStages + 5;
 constexpr int kSmemBytes = 1024 + kBarrierAt + kBarriers * 8 + 32;
 static_assert(kSmemBytes <= 227 * 1024, "stages exceed shared memory");
 constexpr int kScalesAhead = 2;    // own steps whose scale bytes are loaded ahead, in registers
@@ -229,13 +229,14 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr)
 template <int NS>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile uint32_t* failed, uint64_t limit_ns)
 {
+    constexpr uint32_t kLook = NS ? 64 : 1024;   // tries between two looks at the clock and at `failed`
     uint64_t t0 = 0;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
         if (mbar_try_wait(bar, parity))
             return true;
         if (NS)
             __nanosleep(NS);
-        if ((i & 1023) == 1023) {
+        if (i % kLook == kLook - 1) {
             const uint64_t t = global_ns();
             if (!t0)
                 t0 = t;
@@ -248,11 +249,13 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 constexpr int kNow = 0, kSoon = 64, kLater = 500;   // how long a wait sleeps between tries
 
+// Longest wait for what is still under way when a CTA ends.
+constexpr uint64_t kDrainNs = 1000 * 1000 * 1000;
+
 // Before a CTA ends: waits until the copies last issued for each of the `armed`
 // stages have landed.  After a wait has run out these barriers may never
 // complete (they count conversions too), so one limit holds for all of them: a
 // copy takes microseconds.
-constexpr uint64_t kDrainNs = 1000 * 1000 * 1000;
 __device__ __forceinline__ void drain_copies(uint32_t bars, uint32_t stages, uint32_t armed, uint32_t phases)
 {
     const uint64_t t0 = global_ns();
@@ -316,6 +319,12 @@ __device__ __forceinline__ void commit_pair(uint32_t bar)
                  ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                  "h"((uint16_t)3)
                  : "memory");
+}
+
+// The same, on this CTA's barrier alone.
+__device__ __forceinline__ void commit_own(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t bars = base + kBarrierAt;
     const uint32_t full = bars, empty = full + 8 * kStages;
     const uint32_t raw_full = empty + 8 * kStages, raw_empty = raw_full + 8 * kRawStages;
-    const uint32_t tmem_full = raw_empty + 8 * kRawStages, tmem_empty = tmem_full + 16;
+    const uint32_t tmem_full = raw_empty + 8 * kRawStages, tmem_empty = tmem_full + 16, drained = tmem_empty + 16;
     uint32_t* words = reinterpret_cast<uint32_t*>(raw + (bars + 8 * kBarriers - smem_u32(raw)));
     volatile uint32_t* failed = words + 1;
     const uint32_t rank = cluster_rank();
@@ -423,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(tmem_full + 8 * b, 1);
             mbar_init(tmem_empty + 8 * b, 2 * kEpilogueWarps);
         }
+        mbar_init(drained, 1);
         mbar_fence_init();
     }
     if (warp == 1) {
@@ -508,6 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 buf ^= 1;
                 buf_phase ^= buf == 0;
             }
+            // The products still under way write the tensor memory that is freed below, and
+            // where a wait has run out the epilogue has not waited for them.
+            commit_own(drained);
+            mbar_wait(drained, 0, kDrainNs);
         }
     } else if (seat.role == kRoleConvert) {
         // conversion: group g takes steps g, g + 2, ...  A thread takes 16 inputs of
