@@ -1,4 +1,5 @@
-"""The weight gradient's kernel when a wait runs out.
+"""The weight gradient's kernel when a wait runs out: what it has not finished
+is NaN, and every element that is not NaN is right.
 
 Its waits are on its own copies and products, which always arrive, so the
 kernel is launched here with arguments of the test's (tests/c/wgrad_waits.cu):
@@ -91,3 +92,30 @@ def test_a_wait_that_runs_out_under_products(run):
         lost = run(dy, q, s, True, old.clone(), wait_ns, one_pair=True)
         assert bool(torch.isnan(lost).any())
         assert torch.equal(run(dy, q, s, True, old.clone(), 10 ** 9, one_pair=True), whole)
+
+
+@pytest.mark.parametrize("short", ["dy", "checkpoint"])
+@pytest.mark.parametrize("tokens,add,pad", [(64, False, 0), (64, True, 3), (450, False, 0)])
+def test_nothing_unfinished_looks_finished(run, short, tokens, add, pad):
+    """Nothing can be multiplied from the first step on: all of dw is NaN, also the third and
+    later tiles of a pair, whose barrier's last phase has the parity that their waits look
+    for; as for tiles stored at once (16 tiles, one pair), so for those cut along the tokens."""
+    outs, ins = 1024, 1000
+    dy, q, s = problem(tokens, outs, ins, "bf16")
+    dw = torch.ones(outs, ins + pad, dtype=torch.bfloat16, device=DEV)[:, :ins]
+    run(dy, q, s, add, dw, SHORT_WAIT_NS, short_dy=short == "dy", short_q=short == "checkpoint",
+        one_pair=tokens == 64)
+    assert bool(torch.isnan(dw).all()), f"{int((~torch.isnan(dw)).sum())} elements look finished"
+
+
+def test_whatever_is_finished_is_right(run):
+    """Waits that run out while products are issued, on tiles of 5 ms: elements are NaN or those
+    of an undisturbed run."""
+    dy, q, s = problem(1_024_000, 1024, 512, "bf16")
+    old = torch.randn(1024, 512, generator=gen(1), device=DEV).bfloat16()
+    whole = run(dy, q, s, True, old.clone(), 10 ** 9, one_pair=True)
+    for wait_ns in (0, 100_000, 1_000_000, 4_000_000):
+        dw = run(dy, q, s, True, old.clone(), wait_ns, one_pair=True)
+        lost = torch.isnan(dw)
+        assert wait_ns > 1_000_000 or bool(lost.any())
+        assert torch.equal(dw[~lost], whole[~lost]), f"wait of {wait_ns} ns"

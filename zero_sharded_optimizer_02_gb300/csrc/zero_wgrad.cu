@@ -25,7 +25,9 @@
 //
 // Every wait is bounded.  One that runs out (it never does in a healthy run)
 // ends the kernel's loops and the tiles not finished become NaN, so that the
-// optimizer step skips the gradient.
+// optimizer step skips the gradient.  A warp that has given up takes no more part
+// in the schedule: it no longer knows the barriers' phases, so it neither waits
+// for nor announces another tile, and what waits for it gives up in its turn.
 #include <cuda.h>
 
 #include <mutex>
@@ -694,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t mine = lane * 2, line = lane / 4 * kTurnPitch + lane % 4 * 16;
         constexpr int kOld = 16, kTurnOld = 8;
         uint32_t buf = 0, buf_phase = 0;
+        bool ok = true;   // once false, for every later unit: see the top of the file
         for (uint32_t u = pair; u < a.plan.units; u += pairs) {
             const Unit t = unit_at(a.plan, u);
             const uint32_t r = rank * kHalf + quarter * 32 + lane;
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 cp_async_commit();
             };
             fetch_old(0);
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed, a.wait_ns));
+            ok = ok && __all_sync(0xFFFFFFFFu, wait_phase<kLater>(tmem_full + 8 * buf, buf_phase, failed, a.wait_ns));
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const float gain = a.gain && i < a.ins ? widen1<DT>(a.gain[i]) : 1.0f;
             for (uint32_t c = 0; c < kTileO; c += 32) {
@@ -778,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0 && ok)
                 arrive_cluster(map_shared(tmem_empty + 8 * buf, 0));
             buf ^= 1;
             buf_phase ^= buf == 0;
