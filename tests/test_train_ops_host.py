@@ -307,3 +307,13 @@ int main(void)
                            "-Wl,-rpath," + os.path.dirname(_abi.LIB_PATH)])
     out = subprocess.check_output([str(exe)], text=True).split()
     assert out[:3] == ["0", "0", "0"] and int(out[3]) > 0 and out[4] == "32"
+
+
+def test_token_numbers_are_signed_whole_numbers(z):
+    """Other elements of 4 or 8 bytes are no token numbers."""
+    for dtype in (torch.complex64, torch.uint32, torch.uint64, torch.float32, torch.float64):
+        with pytest.raises(ValueError):
+            z.ids(torch.zeros(4, dtype=dtype))
+    for dtype, size in ((torch.int32, 4), (torch.int64, 8)):
+        i = z.ids(torch.zeros(2, 3, dtype=dtype))
+        assert (i.count, i.bytes) == (6, size)

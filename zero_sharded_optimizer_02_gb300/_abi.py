@@ -447,7 +447,8 @@ def mat(t) -> Mat:
 def ids(t) -> Ids:
     """Descriptor of a contiguous int32/int64 torch tensor of token numbers
     (any shape; its elements in order).  It borrows t's memory."""
-    if t.element_size() not in (4, 8) or t.is_floating_point() or not t.is_contiguous():
+    import torch
+    if t.dtype not in (torch.int32, torch.int64) or not t.is_contiguous():
         raise ValueError(f"ids: a contiguous int32 or int64 tensor is needed, not {t.dtype} of "
                          f"strides {tuple(t.stride())}")
     return Ids(t.data_ptr() or None, t.numel(), t.element_size())
