@@ -317,3 +317,54 @@ def test_token_numbers_are_signed_whole_numbers(z):
     for dtype, size in ((torch.int32, 4), (torch.int64, 8)):
         i = z.ids(torch.zeros(2, 3, dtype=dtype))
         assert (i.count, i.bytes) == (6, size)
+
+
+def test_vectors_of_another_type_or_size(z):
+    """A tensor that is not what the kernels read or write at its address is refused before
+    the library sees it: the matrices are at made-up addresses, and nothing is launched."""
+    good = dict(gain=torch.zeros(64, dtype=torch.float16), rstd=torch.zeros(10), ws=torch.zeros(1 << 20, dtype=torch.uint8),
+                bad=torch.zeros(1, dtype=torch.int32))
+    half, wide = torch.zeros(64, dtype=torch.float16), torch.zeros(128, dtype=torch.float16)
+    bad_gains = (half.float(), half.bfloat16(), half[:63], wide[::2], half.short())
+    bad_rstds = (torch.zeros(10, dtype=torch.float16), torch.zeros(10, dtype=torch.float64), torch.zeros(9),
+                 torch.zeros(20)[::2])
+    bad_spaces = (good["ws"][:99], torch.zeros(49, dtype=torch.int16), good["ws"][::2])
+
+    def value_error(fn, args):
+        with pytest.raises(ValueError):
+            fn(*args)
+
+    for g in bad_gains:
+        value_error(z.zero_norm_forward, forward_args(z, gain=g))
+        value_error(z.zero_norm_backward, backward_args(z, gain=g))
+        value_error(z.zero_norm_backward, backward_args(z, dg=g))
+        value_error(z.zero_act_weight_grad, wgrad_args(z, gain=g))
+    for r in bad_rstds:
+        value_error(z.zero_norm_forward, forward_args(z, rstd=r))
+        value_error(z.zero_norm_backward, backward_args(z, rstd=r))
+    for w in bad_spaces:
+        for fn, args in ((z.zero_embed_grad, egrad_args), (z.zero_norm_backward, backward_args),
+                         (z.zero_act_weight_grad, wgrad_args)):
+            value_error(fn, args(z, ws=w, n=100 if w.is_contiguous() else 1 << 19))
+    for b in (torch.zeros(1, dtype=torch.bool), torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.float16)):
+        value_error(z.zero_embed_lookup, lookup_args(z, bad=b))
+        value_error(z.zero_embed_grad, egrad_args(z, bad=b))
+    # what fits reaches the library, which refuses a misaligned matrix here
+    off = mat(z, A + 2, 10, 64)
+    refused(z, 2, z.zero_norm_forward, *forward_args(z, y=off, gain=good["gain"].view(1, 64), rstd=good["rstd"]))
+    refused(z, 2, z.zero_norm_backward, *backward_args(z, dx=off, gain=torch.zeros(70, dtype=torch.float16),
+                                                       rstd=good["rstd"].view(1, 10), dg=good["gain"], ws=good["ws"],
+                                                       n=1 << 20))
+    refused(z, 2, z.zero_embed_lookup, *lookup_args(z, out=off, bad=good["bad"]))
+    refused(z, 2, z.zero_embed_grad, *egrad_args(z, d_out=off, bad=good["bad"].long(), ws=good["ws"], n=1 << 20))
+    refused(z, 2, z.zero_act_weight_grad, *wgrad_args(z, dy=mat(z, A + 2, 10, 40), gain=good["gain"], ws=good["ws"],
+                                                      n=1 << 20))
+    # neither is anything asked of an address, or of an object that only has one
+    class Address:
+        def data_ptr(self):
+            return at(3)
+
+    refused(z, 2, z.zero_norm_forward, *forward_args(z, y=off, gain=Address(), rstd=at(6)))
+    refused(z, 1, z.zero_norm_forward, *forward_args(z, x=None, gain=good["gain"]))
+    refused(z, 1, z.zero_norm_backward, *backward_args(z, dy=None, gain=good["gain"]))
+    refused(z, 1, z.zero_act_weight_grad, *wgrad_args(z, dw=None, gain=good["gain"]))

@@ -3,7 +3,8 @@
 
 Argument marshalling only: every step of the optimizer runs in the library's
 CUDA kernels.  Pointer arguments accept an int address or any object with a
-``data_ptr()`` method (a torch tensor); ``stream`` accepts an int handle, a
+``data_ptr()`` method (a torch tensor; the training operators check its type
+and size too); ``stream`` accepts an int handle, a
 ``torch.cuda.Stream`` or None (the legacy default stream).  A non-OK status
 raises ``ZeroError``.  There is no fallback: if the library is missing, every
 call raises.
@@ -484,13 +485,52 @@ def _row_pitch(t) -> int:
     return -(-t.shape[1] // 16) * 16
 
 
-def _ref(s):
-    return None if s is None else C.byref(s)
+_TORCH_TYPES = {}   # zero_dtype_t (None: fp32) -> torch type
+
+
+def _torch_types():
+    import torch
+    _TORCH_TYPES.update({ZERO_F16: torch.float16, ZERO_BF16: torch.bfloat16, None: torch.float32})
+    return _TORCH_TYPES
+
+
+def _vec(x, what: str, n: int, code):
+    """The address of a vector of n elements of the type `code` (a zero_dtype_t,
+    or None for fp32).  A torch tensor is checked; an int address, or an object
+    that has nothing but one, says nothing of what lies there and passes."""
+    if x is None:
+        return None
+    try:
+        dtype = x.dtype
+        want = (_TORCH_TYPES or _torch_types()).get(code)
+        if dtype is want and x.numel() >= n and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
+    raise ValueError(f"{what}: at least {n} contiguous elements of {want} are needed, not "
+                     f"{tuple(x.shape)} {dtype} of strides {tuple(x.stride())}")
+
+
+def _bytes(x, what: str, n: int):
+    """The address of n bytes of memory; a torch tensor's size is checked."""
+    if x is None:
+        return None
+    try:
+        if x.nbytes >= n and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
+    raise ValueError(f"{what}: {n} contiguous bytes are needed, not {tuple(x.shape)} {x.dtype} of "
+                     f"strides {tuple(x.stride())}")
+
+
+# Descriptors go to the library by reference, which ctypes does by itself for an
+# argument declared as a pointer; None is a null pointer.
 
 
 def zero_embed_lookup(table: Mat, token_ids: Ids, scale: float, out: Mat, d_bad=None,
                       stream=None) -> None:
-    _check(lib().zero_embed_lookup(_ref(table), _ref(token_ids), scale, _ref(out), _ptr(d_bad),
+    _check(lib().zero_embed_lookup(table, token_ids, scale, out, _bytes(d_bad, "d_bad", 4),
                                    _stream(stream)), "zero_embed_lookup")
 
 
@@ -500,16 +540,19 @@ def zero_embed_grad_workspace(tokens: int, vocab: int, dim: int) -> int:
 
 def zero_embed_grad(d_out: Mat, token_ids: Ids, scale: float, accumulate: bool, d_table: Mat,
                     workspace, workspace_bytes: int, d_bad=None, stream=None) -> None:
-    _check(lib().zero_embed_grad(_ref(d_out), _ref(token_ids), scale, int(accumulate),
-                                 _ref(d_table), _ptr(workspace), workspace_bytes, _ptr(d_bad),
-                                 _stream(stream)), "zero_embed_grad")
+    _check(lib().zero_embed_grad(d_out, token_ids, scale, int(accumulate), d_table,
+                                 _bytes(workspace, "workspace", workspace_bytes),
+                                 workspace_bytes, _bytes(d_bad, "d_bad", 4), _stream(stream)),
+           "zero_embed_grad")
 
 
 def zero_norm_forward(x: Mat, residual: Mat | None, gain, eps: float, h: Mat | None,
                       y: Mat | None, rstd=None, checkpoint: Act8 | None = None,
                       stream=None) -> None:
-    _check(lib().zero_norm_forward(_ref(x), _ref(residual), _ptr(gain), eps, _ref(h), _ref(y),
-                                   _ptr(rstd), _ref(checkpoint), _stream(stream)),
+    if x is None:
+        raise ZeroError(ZERO_ERR_INVALID_ARG, "zero_norm_forward")
+    _check(lib().zero_norm_forward(x, residual, _vec(gain, "gain", x.cols, x.dtype), eps, h, y,
+                                   _vec(rstd, "rstd", x.rows, None), checkpoint, _stream(stream)),
            "zero_norm_forward")
 
 
@@ -520,19 +563,22 @@ def zero_norm_backward_workspace(rows: int, cols: int) -> int:
 def zero_norm_backward(dy: Mat, checkpoint: Act8, rstd, gain, d_residual: Mat | None, dx: Mat,
                        d_gain, accumulate: bool, workspace, workspace_bytes: int,
                        stream=None) -> None:
-    _check(lib().zero_norm_backward(_ref(dy), _ref(checkpoint), _ptr(rstd), _ptr(gain),
-                                    _ref(d_residual), _ref(dx), _ptr(d_gain), int(accumulate),
-                                    _ptr(workspace), workspace_bytes, _stream(stream)),
-           "zero_norm_backward")
+    if dy is None:
+        raise ZeroError(ZERO_ERR_INVALID_ARG, "zero_norm_backward")
+    cols, dtype = dy.cols, dy.dtype
+    _check(lib().zero_norm_backward(dy, checkpoint, _vec(rstd, "rstd", dy.rows, None),
+                                    _vec(gain, "gain", cols, dtype), d_residual, dx,
+                                    _vec(d_gain, "d_gain", cols, dtype), int(accumulate),
+                                    _bytes(workspace, "workspace", workspace_bytes),
+                                    workspace_bytes, _stream(stream)), "zero_norm_backward")
 
 
 def zero_act_pack(x: Mat, out: Act8, stream=None) -> None:
-    _check(lib().zero_act_pack(_ref(x), _ref(out), _stream(stream)), "zero_act_pack")
+    _check(lib().zero_act_pack(x, out, _stream(stream)), "zero_act_pack")
 
 
 def zero_act_unpack(checkpoint: Act8, out: Mat, stream=None) -> None:
-    _check(lib().zero_act_unpack(_ref(checkpoint), _ref(out), _stream(stream)),
-           "zero_act_unpack")
+    _check(lib().zero_act_unpack(checkpoint, out, _stream(stream)), "zero_act_unpack")
 
 
 def zero_act_weight_grad_workspace(tokens: int, outs: int, ins: int) -> int:
@@ -541,6 +587,9 @@ def zero_act_weight_grad_workspace(tokens: int, outs: int, ins: int) -> int:
 
 def zero_act_weight_grad(dy: Mat, x: Act8, gain, accumulate: bool, dw: Mat, workspace,
                          workspace_bytes: int, stream=None) -> None:
-    _check(lib().zero_act_weight_grad(_ref(dy), _ref(x), _ptr(gain), int(accumulate), _ref(dw),
-                                      _ptr(workspace), workspace_bytes, _stream(stream)),
-           "zero_act_weight_grad")
+    if dw is None:
+        raise ZeroError(ZERO_ERR_INVALID_ARG, "zero_act_weight_grad")
+    _check(lib().zero_act_weight_grad(dy, x, _vec(gain, "gain", dw.cols, dw.dtype),
+                                      int(accumulate), dw,
+                                      _bytes(workspace, "workspace", workspace_bytes),
+                                      workspace_bytes, _stream(stream)), "zero_act_weight_grad")
