@@ -19,7 +19,8 @@ pass but 8-bit checkpoints:
 
 The table's gradient is the output layer's weight gradient, onto which the
 lookup's gradient is added.  Matrix products with the weights themselves are
-torch's.
+torch's, on its current stream, which every operator is therefore given: the
+library's own default is the legacy stream, and does not follow torch's.
 """
 from __future__ import annotations
 
@@ -81,6 +82,7 @@ def loss_and_grads(s: Shapes, params: torch.Tensor, row: torch.Tensor, tokens: t
                    targets: torch.Tensor, ws: Workspaces) -> torch.Tensor:
     """The mean cross-entropy of one micro-batch; its gradient is stored in `row`."""
     t, d = tokens.numel(), s.dim
+    st = torch.cuda.current_stream()      # torch's own work between the operators goes there
     scale = math.sqrt(d)
     # activations: rows on 16-byte boundaries, whatever their width
     like = lambda cols: torch.empty(t, -(-cols // 8) * 8, dtype=params.dtype,     # noqa: E731
@@ -92,20 +94,20 @@ def loss_and_grads(s: Shapes, params: torch.Tensor, row: torch.Tensor, tokens: t
     # forward: x is what the last block added, h the residual stream so far
     kept = []
     x, h = like(d), None
-    z.zero_embed_lookup(z.mat(p("table")), ids, scale, z.mat(x))
+    z.zero_embed_lookup(z.mat(p("table")), ids, scale, z.mat(x), stream=st)
     for k in range(s.layers + 1):
         gain = p("gain_out" if k == s.layers else f"gain{k}")
         y, rstd = like(d), torch.empty(t, device="cuda")
         normed = z.act8_empty(t, d)
         new_h = h if h is not None else like(d)          # the sum takes the stream's place
         z.zero_norm_forward(z.mat(x), z.mat(h) if h is not None else None, gain, EPS,
-                            z.mat(new_h), z.mat(y), rstd, z.act8(*normed))
+                            z.mat(new_h), z.mat(y), rstd, z.act8(*normed), st)
         h = new_h
         if k == s.layers:
             break
         u = y @ p(f"up{k}").t()
         hidden = z.act8_empty(t, s.hidden)
-        z.zero_act_pack(z.mat(u), z.act8(*hidden))
+        z.zero_act_pack(z.mat(u), z.act8(*hidden), st)
         x = torch.nn.functional.silu(u) @ p(f"down{k}").t()
         kept.append((normed, rstd, hidden))              # y, u and h are not kept
         del y, u
@@ -117,24 +119,24 @@ def loss_and_grads(s: Shapes, params: torch.Tensor, row: torch.Tensor, tokens: t
     soft[torch.arange(t, device="cuda"), targets] -= 1
     d_logits = like(s.vocab)
     d_logits.copy_(soft / t)
-    z.zero_act_weight_grad(z.mat(d_logits), z.act8(*normed), p("gain_out"), False, g("table"), *ws.args)
+    z.zero_act_weight_grad(z.mat(d_logits), z.act8(*normed), p("gain_out"), False, g("table"), *ws.args, stream=st)
     d_y, d_h = d_logits @ p("table"), like(d)
     z.zero_norm_backward(z.mat(d_y), z.act8(*normed), rstd, p("gain_out"), None, z.mat(d_h),
-                         s.view(row, "gain_out"), False, *ws.args)
+                         s.view(row, "gain_out"), False, *ws.args, stream=st)
     for k in reversed(range(s.layers)):                  # d_h: of h behind the block, and of x
         normed, rstd, hidden = kept[k]
         u = like(s.hidden)
-        z.zero_act_unpack(z.act8(*hidden), z.mat(u))
+        z.zero_act_unpack(z.act8(*hidden), z.mat(u), st)
         open_ = torch.sigmoid(u.float())
         a = (u * open_).to(u.dtype)
-        z.zero_act_pack(z.mat(a), z.act8(*hidden))       # in the place of u's
-        z.zero_act_weight_grad(z.mat(d_h), z.act8(*hidden), None, False, g(f"down{k}"), *ws.args)
+        z.zero_act_pack(z.mat(a), z.act8(*hidden), st)   # in the place of u's
+        z.zero_act_weight_grad(z.mat(d_h), z.act8(*hidden), None, False, g(f"down{k}"), *ws.args, stream=st)
         d_u = ((d_h @ p(f"down{k}")) * (open_ + a * (1 - open_))).to(u.dtype)
-        z.zero_act_weight_grad(z.mat(d_u), z.act8(*normed), p(f"gain{k}"), False, g(f"up{k}"), *ws.args)
+        z.zero_act_weight_grad(z.mat(d_u), z.act8(*normed), p(f"gain{k}"), False, g(f"up{k}"), *ws.args, stream=st)
         d_y = d_u @ p(f"up{k}")
         z.zero_norm_backward(z.mat(d_y), z.act8(*normed), rstd, p(f"gain{k}"), z.mat(d_h), z.mat(d_h),
-                             s.view(row, f"gain{k}"), False, *ws.args)
-    z.zero_embed_grad(z.mat(d_h), ids, scale, True, g("table"), *ws.args)
+                             s.view(row, f"gain{k}"), False, *ws.args, stream=st)
+    z.zero_embed_grad(z.mat(d_h), ids, scale, True, g("table"), *ws.args, stream=st)
     return loss
 
 
@@ -152,12 +154,13 @@ def make_group(s: Shapes, nd: int, lr: float, seed: int = 0) -> DataParallelStep
             view.fill_(1.0)
         else:
             view.normal_(0.0, 1.0 / math.sqrt(cols), generator=gen)
+    st = torch.cuda.current_stream()
     for r in dps.ranks:
         n, b = int(dps.layouts[r].length), int(dps.layouts[r].begin)
         zero = torch.zeros(n, device="cuda")
         dps.state[r].load(flat[b:b + n], zero, zero)
         master = dps.state[r].tensors()[0]
-        z.zero_gather_params_shard(master, n, dps.gathered_view(), b, "bf16")
+        z.zero_gather_params_shard(master, n, dps.gathered_view(), b, "bf16", st)
     return dps
 
 

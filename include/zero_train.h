@@ -33,6 +33,9 @@
  *     ..._workspace function gives, 16-byte aligned, overwritten; calls that
  *     may run at the same time need workspaces of their own.
  *   - Work is programmatic dependent launches as in zero.h (ZERO_PDL).
+ *   - stream NULL is the legacy default stream, as in zero.h.  It orders nothing
+ *     with a non-blocking stream, such as another library's current one: pass
+ *     the stream on which the inputs are made and the outputs are used.
  */
 #ifndef ZERO_TRAIN_H
 #define ZERO_TRAIN_H

@@ -73,3 +73,33 @@ def test_training_lowers_the_loss(ex):
     losses = ex.train(steps=40, vocab=300, dim=128, hidden=256, layers=1, tokens=256, nd=2, lr=4e-3,
                       say=lambda *a: None)
     assert losses[0] > 4.0 and losses[-1] < 0.5 * losses[0], losses
+
+
+def test_on_a_stream_of_the_callers(ex):
+    """Captured in a graph on a side stream, where work on any other would be missing: the same
+    loss and gradients.  torch's products may add in another order there; each matrix within twice the
+    rounding of its 16-bit elements."""
+    s = ex.Shapes(401, 128, 200, 2)
+    dps = ex.make_group(s, 1, 1e-3)
+    params = dps.gathered_view()[:s.psi]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    tokens = torch.randint(0, s.vocab, (333,), generator=gen, device="cuda")
+    targets = torch.randint(0, s.vocab, (333,), generator=gen, device="cuda")
+    ws = ex.Workspaces(s, 333)
+    row, again = (torch.zeros(s.psi, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want = float(ex.loss_and_grads(s, params, row, tokens, targets, ws))
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        ex.loss_and_grads(s, params, again, tokens, targets, ws)   # loads what is loaded at first use
+    torch.cuda.synchronize()
+    again.zero_()
+    with torch.cuda.graph(graph, stream=side):
+        loss = ex.loss_and_grads(s, params, again, tokens, targets, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(loss) - want) <= 2.0 ** -7 * want
+    for name in s.at:
+        a, b = (s.view(v, name).float() for v in (again, row))
+        assert float((a - b).norm()) <= 2.0 ** -7 * float(b.norm()), name

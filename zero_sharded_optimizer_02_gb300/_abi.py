@@ -427,6 +427,9 @@ def zero_step_shard_unfused_static(g: Grads, L: Layout, s_in: State, s_out: Stat
 
 
 # -- training operators (include/zero_train.h) ---------------------------------
+#
+# stream=None is the legacy default stream here too, whatever torch's current
+# stream is: under torch.cuda.stream(side), pass side.
 
 # Elements of a row that share one scale byte of an 8-bit checkpoint, and the
 # most columns the norm accepts (include/zero_train.h).
