@@ -7,8 +7,10 @@ gathered buffer of ``DataParallelStep``).  For its micro-batch each rank runs
 
     embedding lookup -> residual blocks -> norm -> tied output layer
 
-and writes its gradient, matrix after matrix, into its contribution row, which
-the optimizer step then reduces.  Nothing of a block is kept for the backward
+and writes its gradient, matrix after matrix, straight into its contribution
+row, which the optimizer step then reduces.  (A row holds one shard every
+row_pitch elements.  It is the flat gradient if row_pitch is the shard's own
+length, so the flat buffer is padded to that.)  Nothing of a block is kept for the backward
 pass but 8-bit checkpoints:
 
   - of the normalised rows (written by the norm itself): they serve the norm's
@@ -42,9 +44,10 @@ EPS = 1e-5
 
 class Shapes:
     """The model's matrices and where each lies in the flat buffer (offsets are
-    multiples of 8 elements, so every matrix has 16-byte rows)."""
+    multiples of 8 elements, so every matrix has 16-byte rows), whose length is a
+    multiple of 8 for each of nd shards."""
 
-    def __init__(self, vocab: int, dim: int, hidden: int, layers: int):
+    def __init__(self, vocab: int, dim: int, hidden: int, layers: int, nd: int = 1):
         if dim % 8 or hidden % 8:
             raise ValueError("dim and hidden must be multiples of 8")
         self.vocab, self.dim, self.hidden, self.layers = vocab, dim, hidden, layers
@@ -55,7 +58,7 @@ class Shapes:
         for name, rows, cols in named + [("gain_out", 1, dim)]:
             self.at[name] = (n, rows, cols)
             n += -(-rows * cols // 8) * 8
-        self.psi = n
+        self.psi = -(-n // (8 * nd)) * 8 * nd
 
     def view(self, flat: torch.Tensor, name: str) -> torch.Tensor:
         n, rows, cols = self.at[name]
@@ -168,13 +171,11 @@ def train(steps: int = 60, vocab: int = 1000, dim: int = 256, hidden: int = 512,
           tokens: int = 512, nd: int = 2, lr: float = 2e-3, say=print) -> list:
     """Trains on sequences whose next token is a fixed permutation of the last;
     returns the mean loss of every step."""
-    s = Shapes(vocab, dim, hidden, layers)
+    s = Shapes(vocab, dim, hidden, layers, nd)
     dps = make_group(s, nd, lr)
     pitch = int(dps.layouts[0].row_pitch)
-    rows = torch.zeros(nd, nd * pitch, dtype=torch.bfloat16, device="cuda")
-    # padded-partition layout: with one matrix row per rank, shard r of a row is
-    # its elements [r * pitch, r * pitch + S); the model writes flat elements
-    flat = [torch.empty(s.psi, dtype=torch.bfloat16, device="cuda") for _ in range(nd)]
+    assert nd * pitch == s.psi            # the shards of a row lie end to end
+    rows = torch.zeros(nd, s.psi, dtype=torch.bfloat16, device="cuda")
     desc = {r: z.grads(rows, nd * pitch, r * pitch, nd, "bf16") for r in dps.ranks}
     ws = Workspaces(s, tokens)
     gen = torch.Generator(device="cuda")
@@ -185,10 +186,7 @@ def train(steps: int = 60, vocab: int = 1000, dim: int = 256, hidden: int = 512,
         total = 0.0
         for j in range(nd):
             toks = torch.randint(0, vocab, (tokens,), generator=gen, device="cuda")
-            total = total + loss_and_grads(s, dps.gathered_view()[:s.psi], flat[j], toks, follow[toks], ws)
-            for r in dps.ranks:
-                n, b = int(dps.layouts[r].length), int(dps.layouts[r].begin)
-                rows[j, r * pitch:r * pitch + n].copy_(flat[j][b:b + n])
+            total = total + loss_and_grads(s, dps.gathered_view()[:s.psi], rows[j], toks, follow[toks], ws)
         if dps.step(desc):
             say(f"step {step}: a nonfinite gradient, skipped on every rank")
         losses.append(float(total) / nd)

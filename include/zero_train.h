@@ -15,6 +15,10 @@
  *     pass reads an 8-bit checkpoint of the normalised rows;
  *   - 8-bit activation checkpoints of any matrix, and the weight gradient of a
  *     linear layer taken from one.
+ * A matrix that crosses the end of a shard can be written into a row only where
+ * the row's shards lie end to end: row_pitch equal to shard_elems (pad the flat
+ * buffer until a shard is a multiple of row_align_elems).  Otherwise its gradient
+ * needs a buffer of its own, to be copied into the row shard by shard.
  *
  * Conventions of this header:
  *   - All pointers of device data must be device (or managed) memory of the

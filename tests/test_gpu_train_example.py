@@ -103,3 +103,17 @@ def test_on_a_stream_of_the_callers(ex):
     for name in s.at:
         a, b = (s.view(v, name).float() for v in (again, row))
         assert float((a - b).norm()) <= 2.0 ** -7 * float(b.norm()), name
+
+
+def test_gradients_are_written_into_the_contribution_rows(ex, monkeypatch):
+    """What the operators write is where the step reads: no copy lies between."""
+    rows, written = [], []
+    grads, work = ex.z.grads, ex.loss_and_grads
+    monkeypatch.setattr(ex.z, "grads", lambda base, *a: rows.append(base) or grads(base, *a))
+    monkeypatch.setattr(ex, "loss_and_grads",
+                        lambda s, params, row, *a: written.append((row.data_ptr(), row.nbytes)) or work(s, params, row, *a))
+    ex.train(steps=1, vocab=301, dim=64, hidden=72, layers=1, tokens=50, nd=3, say=lambda *a: None)
+    first = rows[0].data_ptr()
+    assert len(written) == 3
+    for j, (at, n) in enumerate(written):
+        assert at == first + j * rows[0].stride(0) * 2 and n <= rows[0].stride(0) * 2
