@@ -1,6 +1,7 @@
 """Every instance of the training operators' kernels, at sizes that choose it
 (train_rule): rows of every width that a model has, several turns of a CTA, each
-layout of the table gradient; and the sizes of a training micro-batch."""
+layout of the table gradient; checkpoints of the other 16-bit type; and the
+sizes of a training micro-batch."""
 import itertools
 
 import pytest
@@ -98,6 +99,50 @@ def weight_grad(dy, q, s, outs, ins):
     ws = ops.workspace(n)
     z.zero_act_weight_grad(z.mat(dy), z.act8(q, s), None, False, z.mat(dw), ws, n)
     return dw
+
+
+@on_gpu
+def test_weight_grad_of_a_bfloat16_checkpoint_in_binary16():
+    """Its values are rounded to binary16 once: subnormals where steps are under 2^-24 or
+    2^-14 apart, infinities past 65,504; a converting path of its own (steps that binary16
+    does not hold)."""
+    g = ops.gen(61)
+    tokens, outs, ins = 200, 72, 160
+    x = torch.randn(tokens, ins, generator=g, device=DEV)
+    x[:, :32] *= 2.0 ** -18        # steps of about 2^-23, values down to below binary16's least
+    x[:, 32:64] *= 2.0 ** -22
+    x[:, 64:96] *= 2.0 ** 9        # steps of about 2^4
+    x[:, 128:] = x[:, 128:].abs() * 2.0 ** 22 + 2.0 ** 20      # steps of about 2^17: infinite in binary16
+    x = x.bfloat16()
+    q, s = z.act8_empty(tokens, ins)
+    z.zero_act_pack(z.mat(x), z.act8(q, s))
+    assert int(s[:, 1].min()) < 127 - 24 and int(s[:, 4].min()) > 127 + 15 and int(s[:, 2].max()) < 142
+    dy = (torch.rand(tokens, outs, generator=g, device=DEV) + 0.25).half()
+    kept = ref.values(q, s).to(torch.float16).double()
+    assert bool(torch.isinf(kept[:, 128:]).all()) and bool(torch.isfinite(kept[:, :128]).all())
+    dw = weight_grad(dy, q, s, outs, ins)
+    want, size = ref.weight_grad(dy, kept[:, :128], None)
+    err = (tokens + 4) * 2 * ref.E32 * size
+    assert float(want.abs().max()) < 65504
+    ref.assert_within(dw[:, :128], want, ref.U["f16"] * (want.abs() + err) + err + ref.TINY["f16"], "dw")
+    assert bool((dw[:, 128:] == float("inf")).all())
+
+
+@on_gpu
+def test_weight_grad_of_a_binary16_checkpoint_in_bfloat16():
+    """Whole numbers of 7 bits times 2^-24 to 2^9 are exact in bfloat16."""
+    g = ops.gen(62)
+    tokens, outs, ins = 300, 40, 96
+    x = torch.randn(tokens, ins, generator=g, device=DEV)
+    x[:, :32] *= 2.0 ** -18
+    x[:, 32:64] *= 2.0 ** 13
+    q, s = z.act8_empty(tokens, ins)
+    z.zero_act_pack(z.mat(x.half()), z.act8(q, s))
+    dy = (torch.randn(tokens, outs, generator=g, device=DEV)).bfloat16()
+    dw = weight_grad(dy, q, s, outs, ins)
+    want, size = ref.weight_grad(dy, ref.values(q, s), None)
+    err = (tokens + 4) * 2 * ref.E32 * size
+    ref.assert_within(dw, want, ref.U["bf16"] * (want.abs() + err) + err, "dw")
 
 
 @on_gpu
