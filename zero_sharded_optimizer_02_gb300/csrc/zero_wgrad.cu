@@ -532,7 +532,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // 16-byte loads, and its stores, on different banks.
         const uint32_t group = seat.index / kGroupWarps;
         const bool leads = seat.index % kGroupWarps == 0;
-        volatile uint32_t* stopped = words + 2 + group;   // set by the leading warp before the barrier
+        // The step at which the leading warp gave up, plus one; written before that step's
+        // barrier.  A mere flag could be seen one step early by a warp that is late behind
+        // the barrier before: it would leave, and the others wait for it there for ever.
+        volatile uint32_t* stopped = words + 2 + group;
         const uint32_t p = lane / 4, j = lane % 4;
         const uint32_t tok = seat.index % kGroupWarps * 8 + (p / 2 ^ (p & 1) * 5);
         const uint32_t sw = tok & 7;
@@ -544,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // one warp of the group waits, the others for it
             if (leads && !(wait_phase<kNow>(raw_full + 8 * rstage, rphase, failed, a.wait_ns) &&
                            wait_phase<kNow>(empty + 8 * stage, phase ^ 1, failed, a.wait_ns)))
-                *stopped = 1;
+                *stopped = n + 1;
             asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * kGroupWarps) : "memory");
-            if (*stopped)
+            if (*stopped == n + 1)
                 break;
             const uint32_t src = base + kRawAt + rstage * kRawBytes;
             const uint32_t sc = base + kScaleAt + rstage * kScaleBytes + tok * 16 + j / 2 * 8;
