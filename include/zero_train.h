@@ -21,8 +21,8 @@
  * needs a buffer of its own, to be copied into the row shard by shard.
  *
  * Conventions of this header:
- *   - All pointers of device data must be device (or managed) memory of the
- *     current device (ZERO_ERR_INVALID_ARG otherwise).
+ *   - All pointers of device data must be device (or managed) memory
+ *     (ZERO_ERR_INVALID_ARG otherwise) that the current device can reach.
  *   - Arithmetic is in fp32 (products of 16-bit values on the tensor cores
  *     with fp32 sums); each 16-bit result is rounded once, to nearest even.
  *   - Every result is the same, bit for bit, in every run of the same call on
@@ -102,7 +102,8 @@ typedef struct zero_act8 {
  * zero.  table: a parameter matrix [vocab, dim] (a view into the gathered
  * buffer); out: an activation matrix [ids->count, dim] of the same type.
  * scale: finite.  *d_bad |= 1 if a number >= vocab was met (d_bad may be
- * NULL).  At most 2^31 - 1 tokens and table rows (ZERO_ERR_UNSUPPORTED). */
+ * NULL).  At most 2^31 - 1 tokens and table rows (ZERO_ERR_UNSUPPORTED).  A table
+ * without columns is legal: the call does nothing then, and looks at no number. */
 zero_status_t zero_embed_lookup(const zero_mat_t* table, const zero_ids_t* ids, float scale,
                                 const zero_mat_t* out, uint32_t* d_bad, void* stream);
 
@@ -111,7 +112,8 @@ zero_status_t zero_embed_lookup(const zero_mat_t* table, const zero_ids_t* ids, 
  * row v of the table: rows of absent tokens are stored as zero
  * (accumulate = 0) or left untouched (accumulate = 1).  d_out: an activation
  * matrix [ids->count, dim]; d_table: a parameter gradient [vocab, dim] of the
- * same type.  The tokens are sorted by number within the call. */
+ * same type.  The tokens are sorted by number within the call.  A table without
+ * rows or columns is legal: the call does nothing then, and looks at no number. */
 uint64_t zero_embed_grad_workspace(uint64_t tokens, uint64_t vocab, uint64_t dim);
 zero_status_t zero_embed_grad(const zero_mat_t* d_out, const zero_ids_t* ids, float scale,
                               uint32_t accumulate, const zero_mat_t* d_table, void* workspace,

@@ -270,8 +270,10 @@ __global__ void __launch_bounds__(kThreads) k_sort_move(const SortArgs a)
 // * per) of the order so far, a thread I of them.  A pass counts each warp's
 // digits, adds the counts up over warps and, through the other CTAs' shared
 // memory, over CTAs, and moves every pair to its new place: into the CTA that
-// holds it, or in the last pass to global memory.  The multi-launch passes
-// take about 6 us for each of their launches.
+// holds it, or in the last pass to global memory.  More tokens take the
+// multi-launch passes, and the rows of absent tokens are then written behind the
+// sort: 65,537 tokens x 256 added in 40 us (65,536 in 43), stored 59 (43); x 1,600
+// added 95 (96), stored 106 (94).
 // 65,536 tokens of 50,257 numbers (two passes of 8 bits): 25 us, of which the
 // scattered stores to the other CTAs take 5, ranking 8.  Clusters of 16 CTAs, which
 // not every part of a GPU can hold, took 5 us less there (1 more up to 16,384
@@ -491,17 +493,18 @@ __global__ void __launch_bounds__(kThreads) k_sort_count_all(const ClusterSort a
 
 // -- rows of absent tokens ------------------------------------------------------------
 
-// Writes zeros to the rows of absent tokens (of a stored gradient) while
-// k_sort_cluster, launched before it, runs on its 8 SMs: it starts with it and
-// ends after it (pdl_end), so the sums that follow find both done.  It starts
-// only when every CTA of the sort has passed the wait for the work before the
-// call, and reads and writes nothing that the sort writes.
+// Writes zeros to the rows of absent tokens (of a stored gradient) while the sort
+// launched before it runs, k_sort_cluster on up to 8 SMs or k_sort_count_all on up
+// to 256 CTAs: it starts with it and ends after it (pdl_end), so the sums that
+// follow find both done.  It starts only when every CTA of the sort has passed the
+// wait for the work before the call (each sort begins with pdl_entry, which waits
+// before it lets dependents start), and reads and writes nothing that the sort
+// writes.
 //
 // CTA `me` takes every kZeroCtas-th group of 32 rows, since the rows of absent
 // tokens crowd at one end of a vocabulary sorted by frequency and one SM writes
 // only about 25 bytes a clock.  It marks its tokens by reading all numbers.
-// A thread takes a row (zero_row).  All SMs
-// write at most 4.0 TB/s (a memset of 1 GB), 0.6 of what a copy moves.
+// A thread takes a row (zero_row).  All SMs write at most 4.0 TB/s (a memset of 1 GB), 0.6 of what a copy moves.
 constexpr uint32_t kZeroCtas = 128;
 constexpr int kZeroThreads = 1024;
 constexpr uint32_t kZeroBytes = 8192;
@@ -587,7 +590,8 @@ __global__ void __launch_bounds__(kZeroThreads) k_embed_absent(const ZeroArgs a)
 //   20,000 x 256   27, 28, 31       20,000 x 1,600  59, 54, 55 (stored)
 //   24,000 x 1,600 60, 54, 50       65,536 x 768    76, 68, 61
 //   65,536 x 256   47, 46, 43       65,536 x 1,600  134, 112, 101
-// Only long batches of narrow rows lose: 24,000 x 256 28, 30, 32.
+// Only long batches of narrow rows lose: 24,000 x 256 28, 30, 32.  kSome and kMany
+// keep three CTAs an SM by spilling 8 to 48 bytes a thread.
 enum Layout { kFew, kSome, kMany };
 template <int LAYOUT>
 constexpr int kCellOf = LAYOUT == kMany ? 32 : 16;

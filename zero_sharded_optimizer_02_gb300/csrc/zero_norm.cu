@@ -49,7 +49,10 @@ struct NormLimits {
     static constexpr int threads = V == 1 ? (int)kNormGroup : (int)(WIDE ? kNormWideGroup : kNormMidGroup);
     // CTAs an SM that the registers are limited for.  16,384 x 4,096: forward
     // 101 us with 2, 98 with 3 (x 1,600: 52, 46); backward 117 with 3, 95 with 2,
-    // 145 with 1 (more than two spill).
+    // 145 with 1 (more than two spill; four vectors spill 52 to 64 bytes with two).
+    // WIDE: 1,024 threads leave 64 registers, of which the backward kernel spills
+    // about 750 bytes, and no room for a row ahead: 2,048 x 16,384 forward 54 us
+    // (5.7 TB/s), backward 141 (1.7 TB/s), where 4,096 x 8,192 take 53 and 63.
     static constexpr int ctas = WIDE ? 1 : V == 1 || BACK ? 2 : 3;
     static constexpr int ahead = V == 1 ? 3 : WIDE ? 0 : 1;   // rows
 };

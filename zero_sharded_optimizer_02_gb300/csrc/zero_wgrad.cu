@@ -19,7 +19,8 @@
 // Tiles that would leave pairs idle in the last wave are cut along the tokens
 // into `splits` parts each, whose fp32 sums a second launch adds in order.
 //
-// 16,384 tokens, 4,096 -> 16,384: 1.46 to 1.51 ms, 1.48 PFLOP/s; bound by the
+// 16,384 tokens, 4,096 -> 16,384: 1.46 to 1.51 ms, 1.48 PFLOP/s (a library product of
+// two 16-bit matrices of that shape 1.09 to 1.20 ms, behind an unpack 1.20); bound by the
 // shared-memory pipe (92% busy), which carries the operands to the tensor cores,
 // the bytes to the converting warps and their values back.
 //
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_wait(drained, 0, kDrainNs);
         }
     } else if (seat.role == kRoleConvert) {
-        // conversion: group g takes steps g, g + 2, ...  A thread takes 16 inputs of
+        // conversion: group g takes steps g, g + kGroups, ...  A thread takes 16 inputs of
         // either half at tokens tok and tok + 32.  Lanes 0..3 and 4..7 of a quarter
         // warp take tokens that differ in bits 0 and 2, whose swizzles keep its
         // 16-byte loads, and its stores, on different banks.
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t sc = base + kScaleAt + rstage * kScaleBytes + tok * 16 + j / 2 * 8;
             const uint32_t dst = base + stage * kOperandBytes;
             // Rolled: the loop body then stays in the warp scheduler's instruction
-            // cache, which twenty warps in five roles otherwise thrash.
+            // cache, which 23 warps in six roles otherwise thrash.
 #pragma unroll 1
             for (uint32_t h = 0; h < 2; ++h) {   // tokens tok, tok + 32
                 uint32_t s0, s1;
