@@ -169,7 +169,7 @@ zero_status_t zero_act_unpack(const zero_act8_t* in, const zero_mat_t* out, void
  * checkpoint that zero_act_pack wrote); dw: a parameter gradient [outs, ins]
  * of dy's type.  At most 2^30 tokens, 2^28 outs and ins (ZERO_ERR_UNSUPPORTED);
  * element offsets may pass 2^32.  The kernel's waits on its own copies and
- * products are bounded (4 s each, and 1 s for its copies to land before it ends);
+ * products are bounded (4 s each, and 1 s for those still under way when it ends);
  * should one ever run out, the part of dw not finished is NaN, so that the
  * optimizer step skips the gradient. */
 uint64_t zero_act_weight_grad_workspace(uint64_t tokens, uint64_t outs, uint64_t ins);
