@@ -14,7 +14,10 @@
  *   - the residual addition with the root-mean-square norm, whose backward
  *     pass reads an 8-bit checkpoint of the normalised rows;
  *   - 8-bit activation checkpoints of any matrix, and the weight gradient of a
- *     linear layer taken from one.
+ *     linear layer taken from one;
+ *   - the losses behind the output layer, with the gradient of its logits: token
+ *     log-probabilities, cross-entropy and distillation, policy and preference
+ *     losses.
  * A matrix that crosses the end of a shard can be written into a row only where
  * the row's shards lie end to end: row_pitch equal to shard_elems (pad the flat
  * buffer until a shard is a multiple of row_align_elems).  Otherwise its gradient
@@ -176,6 +179,92 @@ uint64_t zero_act_weight_grad_workspace(uint64_t tokens, uint64_t outs, uint64_t
 zero_status_t zero_act_weight_grad(const zero_mat_t* dy, const zero_act8_t* x, const void* gain,
                                    uint32_t accumulate, const zero_mat_t* dw, void* workspace,
                                    uint64_t workspace_bytes, void* stream);
+
+/* ---- Losses behind the output layer ------------------------------------------------ */
+
+/* Conventions of this section.
+ *   - logits: an activation matrix [tokens, vocab], 1 <= vocab <= ZERO_LOSS_MAX_VOCAB
+ *     (ZERO_ERR_UNSUPPORTED above).  A logit of -inf is an entry that cannot be
+ *     chosen: its probability and its gradient are zero.  A row that holds a NaN or
+ *     +inf, or nothing but -inf, gives NaN.
+ *   - targets: one token number a row.  A row whose target is padding is left out:
+ *     its logits and its other inputs do not count, its loss and log-probability
+ *     are 0 and its row of d_logits is zero.  *d_bad |= 1 if a number >= vocab was
+ *     met (d_bad may be NULL).
+ *   - temperature T: 2^-20 <= T <= 2^20; p = softmax(logits[t] / T) and lp, the
+ *     target's log-probability, are taken at it.
+ *   - d_logits: an activation matrix of the logits' shape and type, the gradient of
+ *     the sum of the losses times `scale` (finite), every row of it written.  It may
+ *     be logits itself (same base and pitch), and NULL where only the loss is wanted.
+ *   - fp32 vectors have one element a row and are 4-byte aligned.
+ *   - The target is left out of the sum that 1 - p[target] is taken from, so that
+ *     loss and gradient keep their relative precision where p is almost 1. */
+#define ZERO_LOSS_MAX_VOCAB 393216u
+
+/* logp[t] = lp and lse[t] = log sum exp(logits[t] / T), both 0 for padding.  Either
+ * may be NULL, not both. */
+zero_status_t zero_token_logprob(const zero_mat_t* logits, const zero_ids_t* targets,
+                                 float temperature, float* logp, float* lse, uint32_t* d_bad,
+                                 void* stream);
+
+/* Its gradient: d_logits[t] = d_logp[t] / T * (one at the target - p). */
+zero_status_t zero_token_logprob_backward(const zero_mat_t* logits, const zero_ids_t* targets,
+                                          float temperature, const float* d_logp,
+                                          const zero_mat_t* d_logits, uint32_t* d_bad,
+                                          void* stream);
+
+/* Most teacher entries a row. */
+#define ZERO_DISTILL_MAX_TOP 256u
+
+/* Distillation from a teacher's top logits, mixed with the ordinary cross-entropy:
+ *     q = softmax(top[t] / T) over the row's present entries
+ *     loss[t] = weight[t] * (soft * T^2 * sum over k of q_k (log q_k - log p[top_ids[t][k]])
+ *                            - hard * log softmax(logits[t])[target])
+ * The cross-entropy is taken at temperature 1.  Without a teacher (top and top_ids
+ * NULL, or no columns) and with hard = 1 this is the ordinary loss of a language model.
+ * top: an activation matrix [tokens, K], K <= ZERO_DISTILL_MAX_TOP
+ * (ZERO_ERR_UNSUPPORTED above), of the logits' type.  top_ids: K numbers a row, row
+ * after row.  An entry is absent if its number is padding (>= vocab: *d_bad too) or its
+ * logit -inf; a row without present entries has no soft part.  Entries of the same
+ * number count each.  targets may be NULL if hard is 0: no row is padding then.
+ * soft, hard: finite.  weight may be NULL (ones).  loss, d_logits: one at least. */
+zero_status_t zero_distill_loss(const zero_mat_t* logits, const zero_mat_t* top,
+                                const zero_ids_t* top_ids, float temperature, float soft,
+                                const zero_ids_t* targets, float hard, const float* weight,
+                                float scale, float* loss, const zero_mat_t* d_logits,
+                                uint32_t* d_bad, void* stream);
+
+/* A clipped policy loss with a KL term to a reference model.  With r = exp(lp -
+ * old_logp[t]), A = advantage[t], d = ref_logp[t] - lp:
+ *     loss[t] = weight[t] * (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                            + kl * (exp(d) - d - 1))
+ * On a clipped row (the second argument is the smaller) only the KL term has a
+ * gradient.  0 <= clip_low <= 1, clip_high >= 0, kl finite.  ref_logp may be NULL if
+ * kl is 0 and is not looked at then; weight may be NULL (ones).  loss, logp (lp) and
+ * d_logits may be NULL, not all three. */
+zero_status_t zero_policy_loss(const zero_mat_t* logits, const zero_ids_t* targets,
+                               float temperature, const float* old_logp, const float* ref_logp,
+                               const float* advantage, const float* weight, float clip_low,
+                               float clip_high, float kl, float scale, float* loss, float* logp,
+                               const zero_mat_t* d_logits, uint32_t* d_bad, void* stream);
+
+/* A preference loss on pairs of sequences.  starts: 2 * pairs + 1 rising row numbers;
+ * sequence i is the rows starts[i] to starts[i + 1] - 1 (none if they are equal), 2j the
+ * chosen and 2j + 1 the rejected one of pair j.  Rows of no sequence are left out as
+ * padding is.  With s_i = sum of logp[t] - ref_logp[t] over the rows of sequence i that
+ * are not padding (in 64 bits; ref_logp NULL: zeros) and m = beta * (s_2j - s_2j+1):
+ *     loss[j] = -(1 - smoothing) * log sigmoid(m) - smoothing * log sigmoid(-m)
+ *     reward[i] = beta * s_i
+ * Log-probabilities are taken at temperature 1.  beta finite, 0 <= smoothing <= 1.
+ * loss: fp32[pairs]; reward: fp32[2 * pairs] or NULL; logp: fp32[tokens] or NULL;
+ * d_logits may be NULL.  A pair whose numbers do not rise, or pass the rows, has a NaN
+ * loss, reward and gradient, so that the optimizer step skips it, and sets *d_bad. */
+uint64_t zero_preference_loss_workspace(uint64_t tokens, uint64_t pairs);
+zero_status_t zero_preference_loss(const zero_mat_t* logits, const zero_ids_t* targets,
+                                   const zero_ids_t* starts, const float* ref_logp, float beta,
+                                   float smoothing, float scale, float* loss, float* reward,
+                                   float* logp, const zero_mat_t* d_logits, void* workspace,
+                                   uint64_t workspace_bytes, uint32_t* d_bad, void* stream);
 
 #ifdef __cplusplus
 }

@@ -112,6 +112,15 @@ _SIGNATURES = {
     "zero_act_unpack": ([_PA, _PM, vp], i32),
     "zero_act_weight_grad_workspace": ([u64, u64, u64], u64),
     "zero_act_weight_grad": ([_PM, _PA, vp, u32, _PM, vp, u64, vp], i32),
+    "zero_token_logprob": ([_PM, _PI, C.c_float, vp, vp, vp, vp], i32),
+    "zero_token_logprob_backward": ([_PM, _PI, C.c_float, vp, _PM, vp, vp], i32),
+    "zero_distill_loss": ([_PM, _PM, _PI, C.c_float, C.c_float, _PI, C.c_float, vp, C.c_float, vp,
+                           _PM, vp, vp], i32),
+    "zero_policy_loss": ([_PM, _PI, C.c_float, vp, vp, vp, vp, C.c_float, C.c_float, C.c_float,
+                          C.c_float, vp, vp, _PM, vp, vp], i32),
+    "zero_preference_loss_workspace": ([u64, u64], u64),
+    "zero_preference_loss": ([_PM, _PI, _PI, vp, C.c_float, C.c_float, C.c_float, vp, vp, vp, _PM,
+                              vp, u64, vp, vp], i32),
 }
 
 # Most contribution rows a gradient descriptor may name (include/zero.h).
@@ -431,10 +440,13 @@ def zero_step_shard_unfused_static(g: Grads, L: Layout, s_in: State, s_out: Stat
 # stream=None is the legacy default stream here too, whatever torch's current
 # stream is: under torch.cuda.stream(side), pass side.
 
-# Elements of a row that share one scale byte of an 8-bit checkpoint, and the
-# most columns the norm accepts (include/zero_train.h).
+# Elements of a row that share one scale byte of an 8-bit checkpoint, the most
+# columns the norm accepts, the widest rows of logits and the most teacher entries
+# a row (include/zero_train.h).
 ZERO_ACT8_BLOCK = 32
 ZERO_NORM_MAX_COLS = 32768
+ZERO_LOSS_MAX_VOCAB = 393216
+ZERO_DISTILL_MAX_TOP = 256
 
 
 def mat(t) -> Mat:
@@ -596,3 +608,71 @@ def zero_act_weight_grad(dy: Mat, x: Act8, gain, accumulate: bool, dw: Mat, work
                                       int(accumulate), dw,
                                       _bytes(workspace, "workspace", workspace_bytes),
                                       workspace_bytes, _stream(stream)), "zero_act_weight_grad")
+
+
+def _rows(m: Mat | None, where: str) -> int:
+    if m is None:
+        raise ZeroError(ZERO_ERR_INVALID_ARG, where)
+    return m.rows
+
+
+def zero_token_logprob(logits: Mat, targets: Ids, temperature: float, logp, lse=None, d_bad=None,
+                       stream=None) -> None:
+    n = _rows(logits, "zero_token_logprob")
+    _check(lib().zero_token_logprob(logits, targets, temperature, _vec(logp, "logp", n, None),
+                                    _vec(lse, "lse", n, None), _bytes(d_bad, "d_bad", 4),
+                                    _stream(stream)), "zero_token_logprob")
+
+
+def zero_token_logprob_backward(logits: Mat, targets: Ids, temperature: float, d_logp,
+                                d_logits: Mat, d_bad=None, stream=None) -> None:
+    n = _rows(logits, "zero_token_logprob_backward")
+    _check(lib().zero_token_logprob_backward(logits, targets, temperature,
+                                             _vec(d_logp, "d_logp", n, None), d_logits,
+                                             _bytes(d_bad, "d_bad", 4), _stream(stream)),
+           "zero_token_logprob_backward")
+
+
+def zero_distill_loss(logits: Mat, top: Mat | None, top_ids: Ids | None, temperature: float,
+                      soft: float, targets: Ids | None, hard: float, weight, scale: float, loss,
+                      d_logits: Mat | None, d_bad=None, stream=None) -> None:
+    n = _rows(logits, "zero_distill_loss")
+    _check(lib().zero_distill_loss(logits, top, top_ids, temperature, soft, targets, hard,
+                                   _vec(weight, "weight", n, None), scale,
+                                   _vec(loss, "loss", n, None), d_logits,
+                                   _bytes(d_bad, "d_bad", 4), _stream(stream)),
+           "zero_distill_loss")
+
+
+def zero_policy_loss(logits: Mat, targets: Ids, temperature: float, old_logp, ref_logp, advantage,
+                     weight, clip_low: float, clip_high: float, kl: float, scale: float, loss,
+                     logp=None, d_logits: Mat | None = None, d_bad=None, stream=None) -> None:
+    n = _rows(logits, "zero_policy_loss")
+    _check(lib().zero_policy_loss(logits, targets, temperature, _vec(old_logp, "old_logp", n, None),
+                                  _vec(ref_logp, "ref_logp", n, None),
+                                  _vec(advantage, "advantage", n, None),
+                                  _vec(weight, "weight", n, None), clip_low, clip_high, kl, scale,
+                                  _vec(loss, "loss", n, None), _vec(logp, "logp", n, None),
+                                  d_logits, _bytes(d_bad, "d_bad", 4), _stream(stream)),
+           "zero_policy_loss")
+
+
+def zero_preference_loss_workspace(tokens: int, pairs: int) -> int:
+    return int(lib().zero_preference_loss_workspace(tokens, pairs))
+
+
+def zero_preference_loss(logits: Mat, targets: Ids, starts: Ids, ref_logp, beta: float,
+                         smoothing: float, scale: float, loss, reward, logp,
+                         d_logits: Mat | None, workspace, workspace_bytes: int, d_bad=None,
+                         stream=None) -> None:
+    n = _rows(logits, "zero_preference_loss")
+    if starts is None:
+        raise ZeroError(ZERO_ERR_INVALID_ARG, "zero_preference_loss")
+    pairs = starts.count // 2
+    _check(lib().zero_preference_loss(logits, targets, starts, _vec(ref_logp, "ref_logp", n, None),
+                                      beta, smoothing, scale, _vec(loss, "loss", pairs, None),
+                                      _vec(reward, "reward", 2 * pairs, None),
+                                      _vec(logp, "logp", n, None), d_logits,
+                                      _bytes(workspace, "workspace", workspace_bytes),
+                                      workspace_bytes, _bytes(d_bad, "d_bad", 4),
+                                      _stream(stream)), "zero_preference_loss")

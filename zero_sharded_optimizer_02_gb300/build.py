@@ -32,6 +32,8 @@ SOURCES = {
                      "-Xptxas", "-v", "-I", INCLUDE, "-c"],
     "zero_wgrad.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
                       "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_loss.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                     "-Xptxas", "-v", "-I", INCLUDE, "-c"],
     "zero_train_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I",
                             INCLUDE, "-c"],
     "zero_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE,
