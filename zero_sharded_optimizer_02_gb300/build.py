@@ -34,6 +34,10 @@ SOURCES = {
                       "-Xptxas", "-v", "-I", INCLUDE, "-c"],
     "zero_loss.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
                      "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_loss_f16.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                     "-Xptxas", "-v", "-I", INCLUDE, "-c"],
+    "zero_loss_bf16.cu": ["nvcc", "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+                     "-Xptxas", "-v", "-I", INCLUDE, "-c"],
     "zero_train_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I",
                             INCLUDE, "-c"],
     "zero_host.cpp": ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE,
@@ -89,7 +93,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             f.write(key)
     headers = [os.path.join(INCLUDE, "zero.h"), os.path.join(INCLUDE, "zero_train.h"),
                os.path.join(csrc, "zero_internal.h"), os.path.join(csrc, "zero_train_internal.h"),
-               os.path.join(csrc, "zero_train_device.cuh"),
+               os.path.join(csrc, "zero_train_device.cuh"), os.path.join(csrc, "zero_loss.cuh"),
                os.path.join(csrc, "zero_device.cuh"), os.path.join(csrc, "zero_ring.cuh"),
                os.path.join(csrc, "zero_small.cuh")]
     objs, procs = [], []

@@ -1,0 +1,1142 @@
+// Losses behind the output layer: token log-probabilities, distillation with
+// cross-entropy, policy and preference losses (zero_train.h).
+//
+// Every one of them is the softmax of a row of logits, a few numbers of the row
+// that turn the target's log-probability into a loss and a slope, and the row's
+// gradient a (p_j - [j is the target]), from which distillation takes a q_j more.
+//
+// Exponentials are taken to base 2 at x k - c, with k = log2(e) / T and c the largest
+// x k.  Every sum names the c that it is relative to, so what c was rounded by
+// cancels.  k is taken in two parts in the sums: one fp32 alone is off by up to 2^-25
+// of the distances between logits, always to the same side.  With R the sum over
+// all elements but the target, and e the target's own: p = e / (R + e), 1 - p =
+// R / (R + e) and log p = -log1p(R / e), which all keep their relative precision
+// however near to 1 p is.
+#pragma once
+
+#include "zero_train_device.cuh"
+
+namespace zero {
+
+enum LossOp { kLogp, kSlope, kDistill, kPolicy, kPairs };
+
+struct LossArgs {
+    const uint16_t* logits;
+    uint16_t* grad;
+    uint64_t pitch, grad_pitch;
+    uint32_t rows, vocab;
+    const void* ids;          // NULL: every row is there, without a target
+    const void* starts;       // kLogp: rows outside starts[0], starts[2 pairs] are left out
+    const void* top_ids;
+    uint32_t id_bytes, start_bytes, top_id_bytes;
+    uint32_t pairs;
+    float k, k1;              // log2(e) / T, log2(e)
+    float k_low, k1_low;      // what they lack
+    float temperature;
+    float scale;              // of the gradient, 1 / T in it
+    // inputs and outputs, one a row
+    const float *slope, *old_logp, *ref, *advantage, *weight;
+    float *logp, *lse, *loss;
+    float* logp_low;          // what logp was rounded by, for sums over sequences
+    uint32_t* bad;
+    // policy
+    float low, high, kl;      // 1 - clip_low, 1 + clip_high
+    // distillation
+    const uint16_t* top;
+    uint64_t top_pitch;
+    uint32_t top_n;
+    float soft, hard;         // of the loss
+    // preference: of which sequence a row is, the slope of each, and the flag
+    int32_t* seq;
+    float* seq_slope;
+    uint32_t* seq_bad;
+    float beta, smoothing;
+    float* reward;
+};
+
+// Launches the rows' kernel of an operator: its gradient's (grad) or the one that only
+// reads; with a teacher (top); of two temperatures (dual: 1 any, 2 and 3: T = 2 and 4).
+cudaError_t launch_loss_f16(const LossArgs& a, LossOp op, bool grad, bool top, int dual, void* stream);
+cudaError_t launch_loss_bf16(const LossArgs& a, LossOp op, bool grad, bool top, int dual, void* stream);
+
+namespace {
+
+constexpr uint32_t kNone = 0xFFFFFFFFu;   // no target in the vocabulary
+constexpr float kLn2 = 0.69314712286f, kLn2Low = 5.769999045e-08f;   // ln 2 in two parts, both above 0
+// How far the hardware's 2^x is below the true one on average over a binade, as
+// measured on 2^20 points of each (at most 1.42e-7 on either side).  A sum of many
+// exponentials is low by as much.
+constexpr float kExpLow = 5.0e-8f;
+constexpr float kLowest = -1e30f;         // c of a sum without finite elements
+
+__device__ __forceinline__ int64_t load_id(const void* ids, uint32_t bytes, uint64_t i)
+{
+    return bytes == 8 ? static_cast<const int64_t*>(ids)[i]
+                      : (int64_t) static_cast<const int32_t*>(ids)[i];
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// -- sums of exponentials ---------------------------------------------------------
+
+// What a sum whose largest element is x is taken relative to: a whole number, so
+// that sums relative to different ones are joined by exact powers of two.
+__device__ __forceinline__ float reference(float x, float k) { return fmaxf(ceilf(x * k), kLowest); }
+
+// r = sum of 2^(x k - c); relative to another c by a factor 2^(c - other).
+struct Sum {
+    float c, r;
+};
+
+// What a row's sums come to: over its elements but the target at k and, where the
+// cross-entropy needs another temperature, at k1; and over the teacher's entries,
+// w = sum of 2^(t k - c) and wd = the same times (t - x).
+struct RowSums {
+    Sum s, s1, w;
+    float wd;
+};
+
+// The largest value of a warp's lanes (a NaN only if all are).
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The sum of the first LANES lanes (a power of two) of every such group of lanes.
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float x)
+{
+#pragma unroll
+    for (int m = LANES / 2; m; m >>= 1)
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+    return x;
+}
+
+// a relative to c instead, which is not below its own.
+__device__ __forceinline__ void rebase(Sum& a, float c)
+{
+    a.r *= ex2(a.c - c);
+    a.c = c;
+}
+
+// The sums of all lanes, of which the first LANES hold some, in each of those.
+template <bool DUAL, bool TOP, int LANES>
+__device__ __forceinline__ void join_lanes(RowSums& t)
+{
+    rebase(t.s, warp_max(t.s.c));
+    t.s.r = lane_sum<LANES>(t.s.r);
+    if (DUAL) {
+        rebase(t.s1, warp_max(t.s1.c));
+        t.s1.r = lane_sum<LANES>(t.s1.r);
+    }
+    if (TOP) {
+        const float c = warp_max(t.w.c), f = ex2(t.w.c - c);
+        // what vanishes counts as absent: an infinite distance must not come in with weight 0
+        t.wd = f != 0.0f ? t.wd * f : 0.0f;
+        t.w.r *= f;
+        t.w.c = c;
+        t.w.r = lane_sum<LANES>(t.w.r);
+        t.wd = lane_sum<LANES>(t.wd);
+    }
+}
+
+__device__ __forceinline__ void add_sum(Sum& a, Sum b)
+{
+    const float c = fmaxf(a.c, b.c);
+    a.r = a.r * ex2(a.c - c) + b.r * ex2(b.c - c);
+    a.c = c;
+}
+
+template <bool DUAL, bool TOP>
+__device__ __forceinline__ void add_sums(RowSums& a, const RowSums& b)
+{
+    add_sum(a.s, b.s);
+    if (DUAL)
+        add_sum(a.s1, b.s1);
+    if (TOP) {
+        const float c = fmaxf(a.w.c, b.w.c), fa = ex2(a.w.c - c), fb = ex2(b.w.c - c);
+        a.wd = (fa != 0.0f ? a.wd * fa : 0.0f) + (fb != 0.0f ? b.wd * fb : 0.0f);
+        add_sum(a.w, b.w);
+    }
+}
+
+__device__ __forceinline__ RowSums no_sums()
+{
+    return RowSums{{kLowest, 0.0f}, {kLowest, 0.0f}, {kLowest, 0.0f}, 0.0f};
+}
+
+// -- a row's numbers ----------------------------------------------------------------
+
+// What a row has besides its logits.
+struct RowIn {
+    bool there;       // false: padding, left out
+    uint32_t target;  // kNone: none
+    float a, b, c, d; // kSlope, kPairs: slope; kPolicy: old, ref, advantage, weight; kDistill: weight
+};
+
+// What says whether a row is there, loaded two rows ahead and looked at one row ahead,
+// when the rest of RowIn is loaded: nothing waits for either.
+struct RowId {
+    int64_t id;
+    int32_t seq;
+};
+
+template <int OP>
+__device__ __forceinline__ RowId load_id_of(const LossArgs& a, uint64_t row)
+{
+    RowId r = {-1, -1};
+    if (row < a.rows) {
+        r.id = a.ids ? load_id(a.ids, a.id_bytes, row) : 0;
+        if (OP == kPairs)
+            r.seq = a.seq[row];
+    }
+    return r;
+}
+
+// What holds for all rows of a call: which of them are in sequences, and whether
+// the sequences' numbers are in order.
+struct AllRows {
+    int64_t begin, end;
+    bool bad;
+};
+
+template <int OP>
+__device__ __forceinline__ AllRows load_all(const LossArgs& a)
+{
+    AllRows r = {0, (int64_t)a.rows, false};
+    if (OP == kLogp && a.starts) {
+        r.begin = load_id(a.starts, a.start_bytes, 0);
+        r.end = load_id(a.starts, a.start_bytes, 2ull * a.pairs);
+    }
+    if (OP == kPairs)
+        r.bad = *a.seq_bad != 0;
+    return r;
+}
+
+// flags: this thread reports a number beyond the vocabulary.
+template <int OP>
+__device__ __forceinline__ RowIn load_row(const LossArgs& a, const AllRows& all, uint64_t row, RowId r, bool flags)
+{
+    RowIn in = {false, kNone, 0.0f, 0.0f, 0.0f, 0.0f};
+    bool counts = row < a.rows;
+    if (OP == kLogp)
+        counts = counts && (int64_t)row >= all.begin && (int64_t)row < all.end;
+    if (OP == kPairs)
+        counts = counts && r.seq >= 0;
+    in.there = counts && r.id >= 0 && r.id < (int64_t)a.vocab;
+    if (flags && counts && a.bad && r.id >= (int64_t)a.vocab)
+        atomicOr(a.bad, 1u);
+    if (!in.there)
+        return in;
+    if (a.ids)
+        in.target = (uint32_t)r.id;
+    if (OP == kPairs)
+        in.a = a.seq_slope[r.seq];
+    if (OP == kSlope)
+        in.a = a.slope[row];
+    if (OP == kPolicy) {
+        in.a = a.old_logp[row];
+        in.b = a.ref ? a.ref[row] : 0.0f;
+        in.c = a.advantage[row];
+        in.d = a.weight ? a.weight[row] : 1.0f;
+    }
+    if (OP == kDistill)
+        in.a = a.weight ? a.weight[row] : 1.0f;
+    return in;
+}
+
+// The gradient of an element is g 2^(x k - c) + g1 2^(x k1 - c1), of the target
+// `at`; entry q of the teacher takes gq 2^(t k - cw) from its own.
+struct RowOut {
+    float g, c, g1, c1, at, gq, cw;
+};
+
+// log p of the target with logit x, exponential e relative to c and r the sum of the
+// others': the value and what rounding it lost.  `low`: how far 2^x is low on average
+// (kExpLow).  With r + e = m 2^n, 0.75 <= m < 1.5, log p = ln 2 (x k - (c + n)) - log m,
+// where every product and difference of large values is taken with its rounding.
+__device__ __forceinline__ float2 log_prob(float x, float k, float k_low, float c, float e, float r, float low)
+{
+    if (r < e)
+        return make_float2(-log1pf(r / e), 0.0f);
+    if (x == -INFINITY)   // of a row without any other logit: NaN
+        return make_float2(r > 0.0f ? -INFINITY : __uint_as_float(0x7FC00000u), 0.0f);
+    const float s = r + e;
+    const int n = ((int)__float_as_uint(s) - 0x3F400000) >> 23;
+    const float m = __uint_as_float(__float_as_uint(s) - ((uint32_t)n << 23));
+    const float p = x * k, whole = c + (float)n, d = p - whole, back = d - p;
+    const float q = fmaf(x, k_low, fmaf(x, k, -p)) + ((p - (d - back)) - (whole + back));
+    const float h = d * kLn2;
+    const float rest = (fmaf(q, kLn2, fmaf(d, kLn2Low, fmaf(d, kLn2, -h))) - low) - logf(m);
+    const float v = h + rest + (s - s);   // a sum that is NaN has no m
+    return make_float2(v, rest - (v - h));
+}
+
+// exp(d) - d - 1, from its series where the difference would cancel.
+__device__ __forceinline__ float exp_minus_line(float d)
+{
+    if (fabsf(d) < 0.3f)
+        return 0.5f * d * d * (1.0f + d / 3 * (1.0f + d / 4 * (1.0f + d / 5 * (1.0f + d / 6 * (1.0f + d / 7)))));
+    return expm1f(d) - d;
+}
+
+// The loss and the slope of a clipped policy row with log-probability lp.
+__device__ __forceinline__ float2 policy_row(const LossArgs& a, const RowIn& in, float lp)
+{
+    const float r = expf(lp - in.a), kept = r * in.c, cut = fminf(fmaxf(r, a.low), a.high) * in.c;
+    const bool inside = !(kept > cut);   // of a NaN too, which then reaches loss and gradient
+    float loss = inside ? -kept : -cut, slope = inside ? -kept : 0.0f;
+    if (a.kl != 0.0f) {
+        const float d = in.b - lp;
+        loss = fmaf(a.kl, exp_minus_line(d), loss);
+        slope = fmaf(-a.kl, expm1f(d), slope);
+    }
+    return make_float2(in.d * loss, in.d * slope);
+}
+
+// A row's gradient from its sums and its target's logit (-inf if it has none).
+template <int OP, int DUAL, bool TOP>
+__device__ __forceinline__ RowOut slopes(const LossArgs& a, const RowIn& in, const RowSums& t, float x, bool bad)
+{
+    RowOut o = {};
+    const float e = ex2(fmaf(x, a.k_low, fmaf(x, a.k, -t.s.c))), s = t.s.r + e;
+    o.c = t.s.c;
+    if (OP == kDistill) {
+        // at T: of the teacher; at 1: of the target.  One sum serves both where T is 1.
+        const bool taught = TOP && t.w.r != 0.0f;   // NaN counts as present
+        const float at_t = taught ? a.soft * a.temperature * (in.a * a.scale) : 0.0f, at_1 = a.hard * (in.a * a.scale);
+        o.cw = t.w.c;
+        o.gq = taught ? __fdividef(at_t, t.w.r) : 0.0f;
+        float e1 = e, r1 = t.s.r;
+        if (DUAL) {
+            e1 = ex2(fmaf(x, a.k1_low, fmaf(x, a.k1, -t.s1.c)));
+            r1 = t.s1.r;
+            o.c1 = t.s1.c;
+            o.g = __fdividef(at_t, s);
+            o.g1 = __fdividef(at_1, r1 + e1);
+        } else {
+            o.g = __fdividef(at_t + at_1, s);
+        }
+        o.at = at_t * __fdividef(e, s) - at_1 * __fdividef(r1, r1 + e1);
+        return o;
+    }
+    float slope = bad ? __uint_as_float(0x7FC00000u) : in.a;
+    if (OP == kPolicy)
+        slope = policy_row(a, in, log_prob(x, a.k, a.k_low, t.s.c, e, t.s.r, kExpLow).x).y;
+    const float g = -(slope * a.scale);
+    o.g = __fdividef(g, s);
+    o.at = -g * __fdividef(t.s.r, s);
+    return o;
+}
+
+// A row's other results.
+template <int OP, int DUAL, bool TOP>
+__device__ __forceinline__ void results(const LossArgs& a, uint32_t row, const RowIn& in, const RowSums& t, float x)
+{
+    if (OP != kLogp && OP != kPolicy && OP != kDistill)
+        return;
+    const float e = ex2(fmaf(x, a.k_low, fmaf(x, a.k, -t.s.c))), s = t.s.r + e;
+    if (OP == kDistill) {
+        if (!a.loss)
+            return;
+        float loss = 0.0f;
+        if (TOP && t.w.r != 0.0f && a.soft != 0.0f)
+            loss = a.soft * a.temperature * a.temperature *
+                   (t.wd / t.w.r / a.temperature + kLn2 * ((t.s.c - t.w.c) + (log2f(s) - log2f(t.w.r))));
+        if (a.hard != 0.0f) {
+            const Sum one = DUAL ? t.s1 : t.s;
+            const float e1 = DUAL ? ex2(fmaf(x, a.k1_low, fmaf(x, a.k1, -one.c))) : e;
+            loss -= a.hard * log_prob(x, a.k1, a.k1_low, one.c, e1, one.r, DUAL > 1 ? kExpLow * (1 << (DUAL - 1)) : kExpLow).x;
+        }
+        a.loss[row] = in.a * loss;
+        return;
+    }
+    const float2 lp = log_prob(x, a.k, a.k_low, t.s.c, e, t.s.r, kExpLow);
+    if (a.logp)
+        a.logp[row] = lp.x;
+    if (OP == kLogp && a.logp_low)
+        a.logp_low[row] = lp.y;
+    if (OP == kLogp && a.lse)
+        a.lse[row] = fmaf(t.s.c, kLn2, fmaf(t.s.c, kLn2Low, logf(s) + kExpLow));
+    if (OP == kPolicy && a.loss)
+        a.loss[row] = policy_row(a, in, lp.x).x;
+}
+
+// A row that is left out.
+template <int OP>
+__device__ __forceinline__ void finish_absent(const LossArgs& a, uint32_t row)
+{
+    if ((OP == kLogp || OP == kPolicy) && a.logp)
+        a.logp[row] = 0.0f;
+    if (OP == kLogp && a.lse)
+        a.lse[row] = 0.0f;
+    if (OP == kLogp && a.logp_low)
+        a.logp_low[row] = 0.0f;
+    if ((OP == kDistill || OP == kPolicy) && a.loss)
+        a.loss[row] = 0.0f;
+}
+
+// -- pairs of fp32 values, two to an instruction -----------------------------------------
+
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 pair(float lo, float hi)
+{
+    F2 p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+}
+
+__device__ __forceinline__ float2 both(F2 p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+__device__ __forceinline__ F2 ex2(F2 a)
+{
+    const float2 f = both(a);
+    return pair(ex2(f.x), ex2(f.y));
+}
+
+// -- vectors of logits ----------------------------------------------------------------
+
+template <int DT>
+__device__ __forceinline__ float wide1(uint16_t h)
+{
+    if (DT == ZERO_F16)
+        return __half2float(__ushort_as_half(h));
+    return __uint_as_float((uint32_t)h << 16);
+}
+
+// An element that load_half() brought, looked at no earlier than here.
+template <int DT>
+__device__ __forceinline__ float wide_late(uint32_t& raw)
+{
+    asm volatile("" : "+r"(raw));
+    return wide1<DT>((uint16_t)raw);
+}
+
+template <int DT>
+__device__ __forceinline__ F2 wide2(uint32_t w)
+{
+    if (DT == ZERO_F16) {
+        __half2 h;
+        memcpy(&h, &w, sizeof(h));
+        const float2 f = __half22float2(h);
+        return pair(f.x, f.y);
+    }
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// -- rows on chip ------------------------------------------------------------------------
+
+// A row is held in the shared memory of a cluster of CTAs, an equal piece in each, so
+// that it is read from memory once: every thread copies its own vectors there
+// (cp.async; it waits for its own copies alone), adds up their exponentials, and turns
+// them into gradients from there.  While a row is worked on the next ones of the
+// cluster are on their way into the other buffers.  A row costs one barrier, at
+// which the warps of all the cluster's CTAs give each other their sums.
+struct RowShape {
+    uint32_t ctas;      // of a cluster
+    uint32_t chunk;     // vectors of 8 logits a CTA
+};
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of this CTA's shared word `p` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// The largest of two packed elements each; NaN only if both are.
+template <int DT>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    if (DT == ZERO_F16) {
+        __half2 x, y;
+        memcpy(&x, &a, 4);
+        memcpy(&y, &b, 4);
+        x = __hmax2(x, y);
+        memcpy(&a, &x, 4);
+    } else {
+        __nv_bfloat162 x, y;
+        memcpy(&x, &a, 4);
+        memcpy(&y, &b, 4);
+        x = __hmax2(x, y);
+        memcpy(&a, &x, 4);
+    }
+    return a;
+}
+
+template <int DT>
+__device__ __forceinline__ float larger_half(uint32_t w)
+{
+    return fmaxf(wide1<DT>((uint16_t)w), wide1<DT>((uint16_t)(w >> 16)));
+}
+
+template <int DT>
+constexpr uint16_t kMinusInf = DT == ZERO_F16 ? 0xFC00u : 0xFF80u;
+
+constexpr size_t kMostSmem = 215 * 1024;   // dynamic, beside the static
+constexpr uint32_t kMostCtas = 8;   // of a cluster
+template <int DT>
+__device__ __forceinline__ uint32_t max_of8(uint4 w)
+{
+    return max2<DT>(max2<DT>(w.x, w.y), max2<DT>(w.z, w.w));
+}
+
+// CTAs an SM that the registers are divided among (64 a thread, or 1,024 threads).
+template <int NT>
+constexpr int kResident = NT == 1024 ? 1 : NT == 512 ? 2 : NT == 256 ? 4 : NT == 128 ? 8 : 24;
+
+// What the warps of a cluster tell each other of a row, in R floats: the sums at k,
+// at k1 (DUAL) and over the teacher's entries (TOP).
+template <bool DUAL, bool TOP>
+constexpr int kRecord = TOP ? 8 : DUAL ? 4 : 2;
+
+template <int R>
+struct Record {
+    float f[R];
+
+    __device__ __forceinline__ void set(const RowSums& t, bool dual, bool top)
+    {
+        f[0] = t.s.c;
+        f[1] = t.s.r;
+        if constexpr (R >= 4) {
+            f[2] = dual ? t.s1.c : 0.0f;
+            f[3] = dual ? t.s1.r : 0.0f;
+        }
+        if constexpr (R == 8) {
+            f[4] = t.w.c;
+            f[5] = t.w.r;
+            f[6] = t.wd;
+            f[7] = 0.0f;
+        }
+    }
+    __device__ __forceinline__ void get(RowSums& t, bool dual, bool top) const
+    {
+        t.s = {f[0], f[1]};
+        if constexpr (R >= 4)
+            if (dual)
+                t.s1 = {f[2], f[3]};
+        if constexpr (R == 8) {
+            t.w = {f[4], f[5]};
+            t.wd = f[6];
+        }
+    }
+    __device__ __forceinline__ void store(float* p) const
+    {
+#pragma unroll
+        for (int i = 0; i < R; i += 2)
+            *reinterpret_cast<float2*>(p + i) = make_float2(f[i], f[i + 1]);
+    }
+    __device__ __forceinline__ void load(const float* p)
+    {
+#pragma unroll
+        for (int i = 0; i < R; i += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(p + i);
+            f[i] = v.x;
+            f[i + 1] = v.y;
+        }
+    }
+    // To shared memory of a CTA of the cluster, counted by a barrier there.  (A barrier
+    // of the whole cluster would first wait until this CTA's gradients are in L2.)
+    __device__ __forceinline__ void send(uint32_t at, uint32_t bar) const
+    {
+#pragma unroll
+        for (int i = 0; i < R; i += 2)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at + 4 * i),
+                         "f"(f[i]), "f"(f[i + 1]), "r"(bar)
+                         : "memory");
+    }
+};
+
+constexpr uint64_t kWaitLimit = 1000000000ull;   // of a wait for the cluster's other CTAs, in ns
+
+// Slots of shared memory for a piece of `chunk` vectors.
+template <int NT>
+__host__ __device__ constexpr uint32_t slots_of(uint32_t chunk)
+{
+    return chunk + 8 > NT ? chunk + 8 : NT;
+}
+
+template <int DT, int OP, bool GRAD, bool TOP, int DUAL, int NT>
+__global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs a, const RowShape shape)
+{
+    constexpr int U = DUAL == 1 ? 1 : 2;   // vectors at a time
+    constexpr int W = NT / 32, R = kRecord<DUAL != 0, TOP>;
+    constexpr int SQ = DUAL > 1 ? DUAL - 1 : 0;   // T = 2^SQ: 2^(x k1) is 2^(x k) squared so many times
+    constexpr int kTops = TOP ? (ZERO_DISTILL_MAX_TOP + NT - 1) / NT : 1;   // entries a thread
+    extern __shared__ uint4 b[];   // [chunk + 8]: this CTA's piece of the row
+    __shared__ uint64_t bars[2];
+    __shared__ Record<R> kept[32];   // rows whose results are still to be given
+    __shared__ float kept_x[32];
+    __shared__ uint32_t kept_row[32];
+    __shared__ __align__(16) int32_t top_id[2][TOP ? ZERO_DISTILL_MAX_TOP : 4];
+    __shared__ float top_k[2][TOP ? ZERO_DISTILL_MAX_TOP : 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t ctas = shape.ctas, rank = ctas > 1 ? cluster_rank() : 0;
+    const uint32_t first = blockIdx.x / ctas, step = gridDim.x / ctas;
+    const uint32_t vec0 = rank * shape.chunk;
+    const uint32_t whole = a.vocab / 8;                       // vectors without a ragged end
+    const uint32_t all = (a.vocab + 7) / 8;
+    const uint32_t mine = all > vec0 ? min(all - vec0, shape.chunk) : 0;
+    const uint32_t full = whole > vec0 ? min(whole - vec0, shape.chunk) : 0;
+    const bool ragged = full < mine;
+    const uint32_t slots = max(full + 8, (uint32_t)NT);   // a thread's first slot is always there
+    if (OP == kLogp && a.seq_bad && blockIdx.x == 0 && tid == 0)
+        *a.seq_bad = 0;
+    float* const parts = reinterpret_cast<float*>(b + slots_of<NT>(shape.chunk));   // [2][ctas * W][R]
+    uint32_t phase = 0;   // of either barrier
+    bool failed = false;
+    if (ctas > 1) {
+        if (tid == 0) {
+            mbar_init(smem_u32(&bars[0]), 1);
+            mbar_init(smem_u32(&bars[1]), 1);
+            mbar_fence_init();
+        }
+        cluster_barrier();   // every CTA and its barriers are there before another sends it anything
+    }
+
+    const bool tells = rank == 0 && tid == 0;
+    const auto load_tops = [&](uint64_t row, bool there, int64_t (&id)[kTops]) {
+#pragma unroll
+        for (int i = 0; i < kTops; ++i)
+            id[i] = TOP && there && tid + i * NT < a.top_n
+                        ? load_id(a.top_ids, a.top_id_bytes, row * a.top_n + tid + i * NT) : -1;
+    };
+    // Vector v of the piece is in slot v + shift(row), so that a warp's accesses start on
+    // 128-byte lines of the logits wherever the row does.  Slots below and above the
+    // piece hold -inf.
+    const uint32_t top_n4 = (a.top_n + 3) / 4 * 4;
+    const uint16_t* base = a.logits + 8ull * vec0;
+    const auto shift_of = [&](uint64_t row) {
+        return (uint32_t)(reinterpret_cast<uintptr_t>(base + row * a.pitch) / 16 % 8);
+    };
+    const auto fetch_slot = [&](const uint16_t* z, uint32_t shift, uint32_t v) {   // z: of slot 0
+        if (v - shift < full)
+            cp_async16(b + v, z + 8 * v);
+        else if (ragged && v - shift == full)
+            cp_async16_part(b + v, z + 8 * v, 2 * (a.vocab % 8));
+    };
+    const auto fetch_row = [&](uint64_t row) {
+        const uint32_t shift = shift_of(row);
+        const uint16_t* z = base + row * a.pitch - 8 * shift;
+        for (uint32_t v = tid; v < slots; v += NT)
+            fetch_slot(z, shift, v);
+    };
+    const AllRows all_rows = load_all<OP>(a);
+    RowIn in = load_row<OP>(a, all_rows, first, load_id_of<OP>(a, first), tells);
+    int64_t id[kTops];
+    load_tops(first, in.there, id);
+    if (in.there)
+        fetch_row(first);
+    RowId later = load_id_of<OP>(a, (uint64_t)first + step);
+    // Gradients of the teacher's entries: stored over the row's own once every thread has
+    // written those, which the next row's barrier says.
+    uint16_t* late[kTops];
+    uint32_t late_value[kTops];
+#pragma unroll
+    for (int i = 0; i < kTops; ++i)
+        late[i] = nullptr;
+    const auto store_late = [&]() {
+#pragma unroll
+        for (int i = 0; i < kTops; ++i) {
+            if (late[i])
+                *late[i] = (uint16_t)late_value[i];
+            late[i] = nullptr;
+        }
+    };
+    uint32_t n_kept = 0;
+    const auto give_results = [&]() {
+        __syncwarp();
+        if (lane < n_kept) {
+            const uint32_t row = kept_row[lane];
+            RowSums t = no_sums();
+            kept[lane].get(t, DUAL != 0, TOP);
+            results<OP, DUAL, TOP>(a, row, load_row<OP>(a, all_rows, row, load_id_of<OP>(a, row), false), t, kept_x[lane]);
+        }
+        __syncwarp();
+        n_kept = 0;
+    };
+    uint32_t odd = 0;
+    for (uint64_t row = first; row < a.rows; row += step) {
+        const uint16_t* z = a.logits + row * a.pitch;
+        const uint32_t shift = shift_of(row), shift_next = shift_of(row + step);
+        const uint16_t* z_next = base + (row + step) * a.pitch - 8 * shift_next;   // of slot 0
+        uint16_t* d = GRAD ? a.grad + row * a.grad_pitch : nullptr;
+        // The next launch's CTAs come in as this one's leave, not before: with some that wait
+        // on every SM two calls in a row took 832 us, not 745 (16,384 x 50,257).
+        if (row + step >= a.rows)
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const RowIn next = load_row<OP>(a, all_rows, row + step, later, tells);
+        later = load_id_of<OP>(a, row + 2ull * step);
+        if (!in.there) {
+            int64_t none_id[kTops];
+            load_tops(row + step, next.there, none_id);
+            if (next.there)
+                fetch_row(row + step);
+            if (tells)
+                finish_absent<OP>(a, row);
+            if (GRAD) {
+                for (uint32_t v = tid; v < full; v += NT)
+                    reinterpret_cast<uint4*>(d)[vec0 + v] = make_uint4(0, 0, 0, 0);
+                if (ragged && full % NT == tid)
+                    store8_row<true>(d, 8ull * (vec0 + full), a.vocab, make_uint4(0, 0, 0, 0));
+            }
+            in = next;
+#pragma unroll
+            for (int i = 0; i < kTops; ++i)
+                id[i] = none_id[i];
+            continue;
+        }
+        const uint32_t target = OP == kDistill && a.hard == 0.0f ? kNone : in.target;
+        uint32_t x_raw = load_half(z + (target != kNone ? target : 0), target != kNone, kMinusInf<DT>);
+        uint32_t entry[kTops];
+        uint32_t entry_q_raw[kTops], entry_x_raw[kTops];
+        float entry_q[kTops], entry_x[kTops];
+        if (TOP) {
+#pragma unroll
+            for (int i = 0; i < kTops; ++i) {
+                const uint32_t e = tid + i * NT;
+                const bool one = e < a.top_n;
+                if (one && a.bad && rank == 0 && id[i] >= (int64_t)a.vocab)
+                    atomicOr(a.bad, 1u);
+                // each entry counts in the CTA that has its logit
+                const bool own = one && id[i] >= 8 * (int64_t)vec0 && id[i] < 8 * (int64_t)(vec0 + shape.chunk) &&
+                                 id[i] < (int64_t)a.vocab;
+                entry[i] = own ? (uint32_t)id[i] : kNone;
+                entry_q_raw[i] = load_half(a.top + row * a.top_pitch + (one ? e : 0), one, kMinusInf<DT>);
+                entry_x_raw[i] = load_half(z + (own ? entry[i] : 0), own, 0);
+            }
+        }
+        if (ctas > 1 && tid == 0)
+            mbar_arrive_expect_tx(smem_u32(&bars[odd]), 4 * R * W * ctas);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        // what is no logit, and the target, which its own sum leaves out, count as -inf
+        constexpr uint32_t kTwo = (uint32_t)kMinusInf<DT> << 16 | kMinusInf<DT>;
+        if (tid < shift)
+            b[tid] = make_uint4(kTwo, kTwo, kTwo, kTwo);
+        for (uint32_t v = shift + mine + (NT + tid - (shift + mine) % NT) % NT; v < slots; v += NT)
+            b[v] = make_uint4(kTwo, kTwo, kTwo, kTwo);
+        if (ragged && (shift + full) % NT == tid)
+            for (uint32_t i = a.vocab % 8; i < 8; ++i)
+                reinterpret_cast<uint16_t*>(b + shift + full)[i] = kMinusInf<DT>;
+        const uint32_t at = target / 8 - vec0;
+        const bool owner = target != kNone && target / 8 >= vec0 && at < mine && (at + shift) % NT == tid;
+        if (owner)
+            reinterpret_cast<uint16_t*>(b + shift + at)[target % 8] = kMinusInf<DT>;
+
+        uint32_t top2 = kTwo;
+#pragma unroll 4
+        for (uint32_t v = tid; v < slots; v += NT)
+            top2 = max2<DT>(top2, max_of8<DT>(b[v]));
+        const float top = larger_half<DT>(top2);
+        RowSums t = no_sums();
+        t.s.c = reference(top, a.k);
+        if (DUAL)
+            t.s1.c = SQ ? t.s.c * (1 << SQ) : reference(top, a.k1);
+        const F2 zero = pair(0.0f, 0.0f), k = pair(a.k, a.k), k_low = pair(a.k_low, a.k_low), k1 = pair(a.k1, a.k1);
+        F2 p[2] = {zero, zero}, p1[2] = {zero, zero};
+        const auto add8 = [&](uint4 q) {
+            const F2 c = pair(-t.s.c, -t.s.c), c1 = pair(-t.s1.c, -t.s1.c), k1_low = pair(a.k1_low, a.k1_low);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 y = wide2<DT>(w[i]);
+                const F2 e = ex2(fma2(y, k_low, fma2(y, k, c))), e2 = SQ > 1 ? mul2(e, e) : e;
+                p[i % 2] = add2(p[i % 2], e);
+                if (SQ)
+                    p1[i % 2] = fma2(e2, e2, p1[i % 2]);
+                else if (DUAL)
+                    p1[i % 2] = add2(p1[i % 2], ex2(fma2(y, k1_low, fma2(y, k1, c1))));
+            }
+        };
+        const bool refill = next.there;
+        // Between a thread's first slot and the last 8 every slot holds a whole vector of any
+        // row, whatever its shift.
+        uint32_t v = tid + NT;
+        add8(b[tid]);
+        if (!GRAD && refill)
+            fetch_slot(z_next, shift_next, tid);
+        if (U == 1)
+            for (; v < full; v += NT) {
+                add8(b[v]);
+                if (!GRAD && refill)
+                    cp_async16(b + v, z_next + 8 * v);
+            }
+        else
+            for (; v + NT < full; v += 2 * NT) {
+                const uint4 w0 = b[v], w1 = b[v + NT];
+                add8(w0);
+                add8(w1);
+                if (!GRAD && refill) {
+                    cp_async16(b + v, z_next + 8 * v);
+                    cp_async16(b + v + NT, z_next + 8 * (v + NT));
+                }
+            }
+        for (; v < slots; v += NT) {
+            add8(b[v]);
+            if (!GRAD && refill)
+                fetch_slot(z_next, shift_next, v);
+        }
+        const F2 r = add2(p[0], p[1]), r1 = add2(p1[0], p1[1]);
+        const float2 rs = both(r), rs1 = both(r1);
+        t.s.r = rs.x + rs.y;
+        if (DUAL)
+            t.s1.r = rs1.x + rs1.y;
+        if (TOP) {
+#pragma unroll
+            for (int i = 0; i < kTops; ++i) {
+                const uint32_t e = tid + i * NT;
+                entry_q[i] = wide_late<DT>(entry_q_raw[i]);
+                entry_x[i] = wide_late<DT>(entry_x_raw[i]);
+                if (e < top_n4) {
+                    const bool here = id[i] >= 0 && id[i] < (int64_t)a.vocab && entry_q[i] != -INFINITY;
+                    if (!here)
+                        entry[i] = kNone;
+                    top_id[odd][e] = here ? (int32_t)id[i] : -1;
+                    top_k[odd][e] = entry_q[i] * a.k;
+                }
+                if (entry[i] != kNone)
+                    t.w.c = fmaxf(t.w.c, reference(entry_q[i], a.k));
+            }
+#pragma unroll
+            for (int i = 0; i < kTops; ++i) {
+                const float w = entry[i] != kNone ? ex2(fmaf(entry_q[i], a.k, -t.w.c)) : 0.0f;
+                if (w != 0.0f) {   // a NaN too
+                    t.w.r += w;
+                    t.wd = fmaf(w, entry_q[i] - entry_x[i], t.wd);
+                }
+            }
+            load_tops(row + step, next.there, id);
+        }
+        join_lanes<DUAL != 0, TOP, 32>(t);
+        if (W > 1 || ctas > 1) {
+            float* const q = parts + odd * (R * W * ctas);
+            const uint32_t n_parts = W * ctas;
+            Record<R> mine_of;
+            mine_of.set(t, DUAL, TOP);
+            bool ok = true;
+            if (ctas == 1) {
+                if (lane == 0)
+                    mine_of.store(q + R * warp);
+                __syncthreads();
+            } else {
+                if (lane < ctas)
+                    mine_of.send(in_cta(q + R * (rank * W + warp), lane), in_cta(&bars[odd], lane));
+                ok = !failed && mbar_wait(smem_u32(&bars[odd]), phase >> odd & 1, kWaitLimit);
+                phase ^= 1u << odd;
+                failed |= !ok;
+            }
+            if (GRAD || warp == 0) {
+                Record<R> r;
+                const uint32_t j = ctas == 1 ? lane % W : lane;
+                t = no_sums();
+                if (j < n_parts) {
+                    r.load(q + R * j);
+                    r.get(t, DUAL, TOP);
+                }
+                for (uint32_t i = lane + 32; i < n_parts; i += 32) {
+                    RowSums o = no_sums();
+                    r.load(q + R * i);
+                    r.get(o, DUAL, TOP);
+                    add_sums<DUAL != 0, TOP>(t, o);
+                }
+                if (ctas == 1)
+                    join_lanes<DUAL != 0, TOP, W>(t);
+                else
+                    join_lanes<DUAL != 0, TOP, 32>(t);
+                if (!ok)
+                    t.s.r = t.s1.r = __uint_as_float(0x7FC00000u);
+            }
+        } else {
+            __syncwarp();   // every lane has read what it needs of the row
+        }
+        if (GRAD && TOP && W > 1) {
+            if (ctas > 1)
+                __syncthreads();   // the cluster's exchange orders no stores
+            store_late();
+        }
+        RowOut o = {};
+        if (GRAD || warp == 0) {
+            const float x = wide_late<DT>(x_raw);
+            if (target != kNone) {   // relative to the target too, where it is the largest
+                rebase(t.s, fmaxf(t.s.c, reference(x, a.k)));
+                if (DUAL)
+                    rebase(t.s1, SQ ? t.s.c * (1 << SQ) : fmaxf(t.s1.c, reference(x, a.k1)));
+            }
+            if (GRAD)
+                o = slopes<OP, DUAL, TOP>(a, in, t, x, all_rows.bad);
+            if (OP != kSlope && OP != kPairs && rank == 0 && warp == 0) {
+                // a row's results cost a warp what those of 32 rows do: they wait for 31 more
+                if (lane == 0) {
+                    kept[n_kept].set(t, DUAL != 0, TOP);
+                    kept_x[n_kept] = x;
+                    kept_row[n_kept] = (uint32_t)row;
+                }
+                if (++n_kept == 32)
+                    give_results();
+            }
+        }
+        if (GRAD) {
+            uint4* out = reinterpret_cast<uint4*>(d) + vec0 - shift;   // of slot 0
+            const F2 g = pair(o.g, o.g), g1 = pair(o.g1, o.g1), c = pair(-o.c, -o.c), c1 = pair(-o.c1, -o.c1);
+            const auto grads = [&](uint4 q) {
+                uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 y = wide2<DT>(w[i]);
+                    const F2 e = ex2(fma2(y, k, c));
+                    F2 d;
+                    if (SQ) {
+                        const F2 e3 = SQ > 1 ? mul2(e, mul2(e, e)) : e;
+                        d = mul2(e, fma2(g1, e3, g));
+                    } else {
+                        d = mul2(g, e);
+                        if (DUAL)
+                            d = fma2(g1, ex2(fma2(y, k1, c1)), d);
+                    }
+                    const float2 f = both(d);
+                    w[i] = narrow2<DT>(f.x, f.y);
+                }
+                return make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            const auto put = [&](uint32_t v, uint4 w) {
+                if (v - shift < full)
+                    out[v] = w;
+                else if (ragged && v - shift == full)
+                    store8_row<true>(d, 8ull * (vec0 + full), a.vocab, w);
+            };
+            put(tid, grads(b[tid]));
+            if (refill)
+                fetch_slot(z_next, shift_next, tid);
+            v = tid + NT;
+            if (U == 1)
+                for (; v < full; v += NT) {
+                    out[v] = grads(b[v]);
+                    if (refill)
+                        cp_async16(b + v, z_next + 8 * v);
+                }
+            else
+                for (; v + NT < full; v += 2 * NT) {
+                    const uint4 w0 = b[v], w1 = b[v + NT];
+                    out[v] = grads(w0);
+                    out[v + NT] = grads(w1);
+                    if (refill) {
+                        cp_async16(b + v, z_next + 8 * v);
+                        cp_async16(b + v + NT, z_next + 8 * (v + NT));
+                    }
+                }
+            for (; v < slots; v += NT) {
+                put(v, grads(b[v]));
+                if (refill)
+                    fetch_slot(z_next, shift_next, v);
+            }
+            if (owner)
+                d[target] = (uint16_t)narrow2<DT>(o.at, 0.0f);
+            if (TOP) {
+#pragma unroll
+                for (int i = 0; i < kTops; ++i) {
+                    if (entry[i] == kNone)
+                        continue;
+                    float sum = 0.0f;   // of all entries of this number, in order
+                    const int32_t e = (int32_t)entry[i];
+                    for (uint32_t j = 0; j < top_n4; j += 4) {
+                        const int4 w = *reinterpret_cast<const int4*>(&top_id[odd][j]);
+                        if (w.x == e)
+                            sum += ex2(top_k[odd][j] - o.cw);
+                        if (w.y == e)
+                            sum += ex2(top_k[odd][j + 1] - o.cw);
+                        if (w.z == e)
+                            sum += ex2(top_k[odd][j + 2] - o.cw);
+                        if (w.w == e)
+                            sum += ex2(top_k[odd][j + 3] - o.cw);
+                    }
+                    float dense = o.g * ex2(fmaf(entry_x[i], a.k, -o.c));
+                    if (DUAL)
+                        dense = fmaf(o.g1, ex2(fmaf(entry_x[i], a.k1, -o.c1)), dense);
+                    if (entry[i] == target)
+                        dense = o.at;
+                    late[i] = d + entry[i];
+                    late_value[i] = narrow2<DT>(fmaf(-o.gq, sum, dense), 0.0f);
+                }
+                if (W == 1) {
+                    __syncwarp();
+                    store_late();
+                }
+            }
+        }
+        in = next;
+        odd ^= 1;
+    }
+    if (n_kept)
+        give_results();
+    if (GRAD && TOP && W > 1) {
+        __syncthreads();
+        store_late();
+    }
+    if (ctas > 1)
+        cluster_barrier();   // none leaves before all have what it sends
+}
+
+// -- launches -------------------------------------------------------------------------------
+
+// How a call's rows are laid on the GPU: CTAs of `threads` threads, `ctas` of them a row.
+struct Layout {
+    uint32_t threads, ctas;
+};
+
+constexpr uint32_t kSmemOfSm = 228 * 1024, kSmemOfCta = 1024;   // an SM's, and what a CTA takes besides its own
+
+uint32_t chunk_of(uint32_t vecs, uint32_t ctas) { return ((vecs + ctas - 1) / ctas + 7) / 8 * 8; }
+
+Layout layout_of(uint32_t vecs, uint32_t rows, uint32_t sms)
+{
+    // the split of a row that fills shared memory best, with two CTAs an SM at least
+    uint32_t ctas = 1;
+    double best = 0.0;
+    for (uint32_t c = 1; c <= kMostCtas; ++c) {
+        const uint32_t bytes = 16 * (chunk_of(vecs, c) + 8) + 6 * 1024;
+        const uint32_t n = kSmemOfSm / bytes;
+        const double fill = (double)(n < 4 ? n : 4) * bytes / (1.0 + 0.05 * c);
+        if (n >= 2 && fill > best) {
+            best = fill;
+            ctas = c;
+        }
+        if (n >= 4)
+            break;
+    }
+    if (rows <= 2 * sms && vecs > 512) {
+        // few rows: over as many SMs as there are
+        while (ctas < kMostCtas && rows * ctas * 2 <= 2 * sms && chunk_of(vecs, ctas) > 512)
+            ctas = ctas <= 2 ? 2 * ctas : ctas <= 4 ? 8 : 8;
+        const uint32_t chunk = chunk_of(vecs, ctas);
+        return Layout{chunk <= 512 ? 128u : chunk <= 1024 ? 256u : 512u, ctas};
+    }
+    if (rows <= 2 * sms)
+        return Layout{vecs <= 64 ? 32u : 128u, 1};
+    return Layout{vecs <= 512 ? 32u : vecs <= 1024 ? 128u : 256u, ctas};
+}
+
+template <int DT, int OP, bool GRAD, bool TOP, int DUAL, int NT>
+cudaError_t launch_shape(const LossArgs& a, uint32_t ctas, uint32_t sms, void* stream)
+{
+    static std::atomic<uint64_t> allowed{0};
+    const auto kernel = k_loss_rows<DT, OP, GRAD, TOP, DUAL, NT>;
+    RowShape sh;
+    sh.ctas = ctas;
+    sh.chunk = chunk_of((a.vocab + 7) / 8, ctas);
+    const size_t smem = 16 * (size_t)slots_of<NT>(sh.chunk) + 2 * 4 * kRecord<DUAL != 0, TOP> * ctas * (NT / 32);
+    allow_smem(kernel, kMostSmem, allowed);
+    uint32_t clusters = 0;
+    if (ctas == 1) {
+        const uint32_t fit = kSmemOfSm / (uint32_t)(smem + kSmemOfCta + 512 + 128 * kRecord<DUAL != 0, TOP> + (TOP ? 4096 : 0));
+        clusters = sms * (fit < kResident<NT> ? fit : kResident<NT>);
+    } else {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim = {ctas, 1, 1};
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess)
+            return e;
+        clusters = (uint32_t)n;
+    }
+    if (clusters > a.rows)
+        clusters = a.rows;
+    return launch_train(kernel, dim3((clusters ? clusters : 1) * ctas), NT, smem, ctas, stream, a, sh);
+}
+
+template <int DT, int OP, bool GRAD, bool TOP = false, int DUAL = 0>
+cudaError_t launch_type(const LossArgs& a, void* stream)
+{
+    const uint32_t sms = (uint32_t)sm_count();
+    if (!sms)
+        return cudaErrorInvalidDevice;
+    const Layout l = layout_of((a.vocab + 7) / 8, a.rows, sms);
+    switch (l.threads) {
+    case 32: return launch_shape<DT, OP, GRAD, TOP, DUAL, 32>(a, l.ctas, sms, stream);
+    case 128: return launch_shape<DT, OP, GRAD, TOP, DUAL, 128>(a, l.ctas, sms, stream);
+    case 256: return launch_shape<DT, OP, GRAD, TOP, DUAL, 256>(a, l.ctas, sms, stream);
+    }
+    return launch_shape<DT, OP, GRAD, TOP, DUAL, 512>(a, l.ctas, sms, stream);
+}
+
+template <int DT, bool GRAD>
+cudaError_t launch_distill(const LossArgs& a, bool top, int dual, void* stream)
+{
+    return !top        ? launch_type<DT, kDistill, GRAD>(a, stream)
+           : dual == 0 ? launch_type<DT, kDistill, GRAD, true, 0>(a, stream)
+           : dual == 2 ? launch_type<DT, kDistill, GRAD, true, 2>(a, stream)
+           : dual == 3 ? launch_type<DT, kDistill, GRAD, true, 3>(a, stream)
+                       : launch_type<DT, kDistill, GRAD, true, 1>(a, stream);
+}
+
+template <int DT>
+cudaError_t launch_loss(const LossArgs& a, LossOp op, bool grad, bool top, int dual, void* stream)
+{
+    switch (op) {
+    case kLogp: return launch_type<DT, kLogp, false>(a, stream);
+    case kSlope: return launch_type<DT, kSlope, true>(a, stream);
+    case kPairs: return launch_type<DT, kPairs, true>(a, stream);
+    case kPolicy: return grad ? launch_type<DT, kPolicy, true>(a, stream) : launch_type<DT, kPolicy, false>(a, stream);
+    case kDistill: break;
+    }
+    return grad ? launch_distill<DT, true>(a, top, dual, stream) : launch_distill<DT, false>(a, top, dual, stream);
+}
+
+}  // namespace
+}  // namespace zero
