@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import loss_ref as ref
+import loss_rule as rule
 import zero_sharded_optimizer_02_gb300 as z
 from train_ref import TYPES
 
@@ -637,22 +638,95 @@ def test_scoring_then_policy_and_pair_steps():
     z.zero_token_logprob(m, t, 1.0, old)
     z.zero_token_logprob(m, t, 1.0, frozen)
     adv = vec(g, 120)
-    loss, lp, d, d_ref = torch.empty(120, device=DEV), torch.empty(120, device=DEV), grad_of(x), grad_of(x)
+    loss, lp, d = torch.empty(120, device=DEV), torch.empty(120, device=DEV), grad_of(x)
     z.zero_policy_loss(m, t, 1.0, old, frozen, adv, None, 0.2, 0.2, 0.1, 4.0, loss, lp, z.mat(d.t))
-    assert torch.equal(lp, old)
+    # the two log-probabilities are sums of the same numbers in two orders
     live = targets >= 0
-    assert torch.equal(loss[live], -adv[live])
-    z.zero_token_logprob_backward(m, t, 1.0, -4.0 * adv, z.mat(d_ref.t))
-    assert torch.equal(d.t, d_ref.t)
+    r = ref.Rows(x, targets.clamp(min=0), 1.0, live)
+    tol = 2 * r.masked(r.lp_tol)
+    assert bool(((lp.double() - old.double()).abs() <= tol).all())
+    # so the ratio is 1 and the KL term's slope 0 to within that; 0.1 is its weight
+    assert bool(((loss.double() + adv.double()).abs()[live] <= (adv.double().abs() * (tol + 2.0 ** -21) + 0.1 * tol)[live]).all())
+    want = ref.logprob_backward(x, targets, 1.0, -4.0 * adv, "f16")
+    extra = 4.0 * (adv.double().abs() * (tol + 2.0 ** -21) + 0.1 * (tol + 2.0 ** -21))[:, None] * (r.p.nan_to_num(0) + 1)
+    near(d.t, (want[0], want[1] + r.masked(extra)), "d_logits")
     starts = starts_of([30, 30, 20, 40])
     pl, rew, ws = torch.empty(2, device=DEV), torch.empty(4, device=DEV), space(z.zero_preference_loss_workspace(120, 2))
     z.zero_preference_loss(m, t, z.ids(starts), frozen, 0.1, 0.0, 4.0, pl, rew, None, z.mat(d.t), ws, ws.numel())
     # the sums take the policy's log-probabilities unrounded, and the frozen model's as they are given: each is off by
-    # half a step of fp32 at most
-    off = [0.1 * 2.0 ** -24 * float(frozen[a:b].double().abs().sum()) for a, b in zip(starts.tolist(), starts.tolist()[1:])]
+    # half a step of fp32 at most; and they may be sums in two orders
+    off = [0.1 * float((2.0 ** -24 * frozen.double().abs() + tol)[a:b].sum()) for a, b in zip(starts.tolist(), starts.tolist()[1:])]
     assert all(abs(r) <= o + 1e-12 for r, o in zip(rew.tolist(), off))
     assert bool(((pl - math.log(2.0)).abs() < 1e-6 + sum(off)).all())
     slope = torch.zeros(120, device=DEV)
     for i, (a, b) in enumerate(zip(starts.tolist(), starts.tolist()[1:])):
         slope[a:b] = -0.05 * 4.0 if i % 2 == 0 else 0.05 * 4.0
-    near(d.t, ref.logprob_backward(x, targets, 1.0, slope, "f16"), "d_logits")
+    want = ref.logprob_backward(x, targets, 1.0, slope, "f16")
+    near(d.t, (want[0], want[1] + r.masked(4.0 * 0.1 * sum(off) * (r.p.nan_to_num(0) + 1))), "d_logits")
+
+
+# -- every instance -----------------------------------------------------------------------
+
+# (rows, vocabulary, layouts of the gradient, with a teacher, of the scores): loss_rule
+MANY = [(700, 40), (700, 4096), (640, 4100), (620, 8300), (610, 32001), (615, 50257), (609, 57000), (612, 100003),
+        (609, 114001), (620, 131072)]
+FEW = [(3, 300), (150, 600), (20, 4100), (9, 8300), (30, 32001), (300, 20000), (64, 57000), (1, 114001), (7, 131072)]
+
+
+def test_the_sizes_run_every_layout():
+    seen = {kind: {rule.layout(r, v, *kind) for r, v in MANY + FEW} for kind in ((True, False), (True, True), (False, False))}
+    for kind, layouts in seen.items():
+        assert {t for t, _ in layouts} == {32, 128, 256, 512}, (kind, layouts)
+        assert {1, 2, 4, 5, 8} <= {c for _, c in layouts}, (kind, layouts)
+    # over clusters, many rows: a CTA takes several, by turns
+    for kind in seen:
+        assert any(rule.layout(r, v, *kind)[1] > 1 for r, v in MANY)
+
+
+@pytest.mark.parametrize("dtype,rows,vocab", [(DTYPES[i % 2], *s) for i, s in enumerate(MANY + FEW)])
+def test_layouts(dtype, rows, vocab):
+    g, x, targets = batch(rows + vocab, rows, vocab, dtype, pad=0.3)
+    check_logprob(x, targets, 1.3)
+    check_distill(x, None, None, 1.0, 0.0, targets, 1.0, None, 2.0, dtype)
+    torch.cuda.empty_cache()
+    top, ids = teacher(g, x, 19)
+    ids[:, 1] = targets
+    for temp in (2.0, 3.0):
+        check_distill(x, top, ids, temp, 0.5, targets, 0.5, None, 2.0, dtype)
+        torch.cuda.empty_cache()
+    d_lp = vec(g, rows, 1.0, targets < 0)
+    d = grad_of(x)
+    z.zero_token_logprob_backward(z.mat(x), z.ids(targets), 1.0, d_lp, z.mat(d.t))
+    z.zero_token_logprob_backward(z.mat(x), z.ids(targets), 1.0, d_lp, z.mat(x))
+    assert torch.equal(x, d.t)
+
+
+@pytest.mark.parametrize("rows,vocab", [(700, 257), (640, 5000), (615, 50257)])
+@pytest.mark.parametrize("temp", [1.0, 2.0, 4.0, 2.7])
+def test_many_rows_with_the_most_entries(rows, vocab, temp):
+    g, x, targets = batch(rows, rows, vocab, "bf16", pad=0.5)
+    top, ids = teacher(g, x, 256)
+    check_distill(x, top, ids, temp, 0.75, targets, 0.25, None, 4.0, "bf16")
+
+
+@pytest.mark.parametrize("rows,vocab", [(700, 257), (640, 5000), (615, 50257), (612, 100003)])
+def test_many_rows_in_pairs(rows, vocab):
+    g, x, targets = batch(rows, rows, vocab, "f16", pad=0.3)
+    lengths = [rows // 5, rows // 7, 0, rows // 3, 1, 1]
+    check_preference(x, targets, starts_of(lengths), vec(g, rows, 1.0, targets < 0) - 5, 0.1, 0.1, 16.0, "f16")
+
+
+def test_logits_that_lie_apart_on_lines():
+    """Rows on every 16-byte boundary of a 128-byte line, and gradients on another than the logits."""
+    rows, vocab = 640, 4111
+    g, x, targets = batch(77, rows, vocab, "f16")
+    buf = torch.empty(64 + rows * 4136, dtype=torch.float16, device=DEV)
+    for off in (0, 8, 24, 56):
+        y = buf[off:off + rows * 4136].view(rows, 4136)[:, :vocab]        # rows 4,136 * 2 = 64 * 129 + 16 bytes apart
+        y.copy_(x)
+        loss, d = torch.empty(rows, device=DEV), grad_of(x)
+        z.zero_distill_loss(z.mat(y), None, None, 1.0, 0.0, z.ids(targets), 1.0, None, 1.0, loss, z.mat(d.t))
+        want_loss, want = ref.distill(y, None, None, 1.0, 0.0, targets, 1.0, None, 1.0, "f16")
+        near(loss, want_loss, "loss")
+        near(d.t, want, "d_logits")
+        d.check()

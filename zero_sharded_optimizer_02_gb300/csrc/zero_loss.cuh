@@ -645,6 +645,9 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
     }
 
     const bool tells = rank == 0 && tid == 0;
+    // The pairs' gradient takes the rows from the last on: those are the ones that the
+    // scores have left in L2.
+    const auto row_of = [&](uint64_t n) { return OP == kPairs && n < a.rows ? a.rows - 1 - n : n; };
     const auto load_tops = [&](uint64_t row, bool there, int64_t (&id)[kTops]) {
 #pragma unroll
         for (int i = 0; i < kTops; ++i)
@@ -672,12 +675,12 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
             fetch_slot(z, shift, v);
     };
     const AllRows all_rows = load_all<OP>(a);
-    RowIn in = load_row<OP>(a, all_rows, first, load_id_of<OP>(a, first), tells);
+    RowIn in = load_row<OP>(a, all_rows, row_of(first), load_id_of<OP>(a, row_of(first)), tells);
     int64_t id[kTops];
-    load_tops(first, in.there, id);
+    load_tops(row_of(first), in.there, id);
     if (in.there)
-        fetch_row(first);
-    RowId later = load_id_of<OP>(a, (uint64_t)first + step);
+        fetch_row(row_of(first));
+    RowId later = load_id_of<OP>(a, row_of((uint64_t)first + step));
     // Gradients of the teacher's entries: stored over the row's own once every thread has
     // written those, which the next row's barrier says.
     uint16_t* late[kTops];
@@ -706,22 +709,23 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
         n_kept = 0;
     };
     uint32_t odd = 0;
-    for (uint64_t row = first; row < a.rows; row += step) {
+    for (uint64_t n = first; n < a.rows; n += step) {
+        const uint64_t row = row_of(n), row_next = row_of(n + step);
         const uint16_t* z = a.logits + row * a.pitch;
-        const uint32_t shift = shift_of(row), shift_next = shift_of(row + step);
-        const uint16_t* z_next = base + (row + step) * a.pitch - 8 * shift_next;   // of slot 0
+        const uint32_t shift = shift_of(row), shift_next = shift_of(row_next);
+        const uint16_t* z_next = base + row_next * a.pitch - 8 * shift_next;   // of slot 0
         uint16_t* d = GRAD ? a.grad + row * a.grad_pitch : nullptr;
         // The next launch's CTAs come in as this one's leave, not before: with some that wait
         // on every SM two calls in a row took 832 us, not 745 (16,384 x 50,257).
-        if (row + step >= a.rows)
+        if (n + step >= a.rows)
             asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        const RowIn next = load_row<OP>(a, all_rows, row + step, later, tells);
-        later = load_id_of<OP>(a, row + 2ull * step);
+        const RowIn next = load_row<OP>(a, all_rows, row_next, later, tells);
+        later = load_id_of<OP>(a, row_of(n + 2ull * step));
         if (!in.there) {
             int64_t none_id[kTops];
-            load_tops(row + step, next.there, none_id);
+            load_tops(row_next, next.there, none_id);
             if (next.there)
-                fetch_row(row + step);
+                fetch_row(row_next);
             if (tells)
                 finish_absent<OP>(a, row);
             if (GRAD) {
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                     t.wd = fmaf(w, entry_q[i] - entry_x[i], t.wd);
                 }
             }
-            load_tops(row + step, next.there, id);
+            load_tops(row_next, next.there, id);
         }
         join_lanes<DUAL != 0, TOP, 32>(t);
         if (W > 1 || ctas > 1) {
@@ -1037,32 +1041,45 @@ constexpr uint32_t kSmemOfSm = 228 * 1024, kSmemOfCta = 1024;   // an SM's, and 
 
 uint32_t chunk_of(uint32_t vecs, uint32_t ctas) { return ((vecs + ctas - 1) / ctas + 7) / 8 * 8; }
 
-Layout layout_of(uint32_t vecs, uint32_t rows, uint32_t sms)
+// grad: of an operator with a gradient, whether it is wanted or not: the loss is the same,
+// bit for bit; top: with a teacher's entries to look at.
+Layout layout_of(uint32_t vecs, uint32_t rows, uint32_t sms, bool grad, bool top)
 {
-    // the split of a row that fills shared memory best, with two CTAs an SM at least
-    uint32_t ctas = 1;
+    // The split of a row that fills shared memory best, with `least` CTAs an SM, whose loads
+    // and sums take turns; more CTAs of a row have to wait for each other.  16,384 x 50,257
+    // with gradient: 521 us unsplit, 552 in two (with a teacher, whose entries are few
+    // threads' work: 330 and 315; scored: 225 and 217).  4,096 x 131,072 with gradient:
+    // 260 in four, 302 in three, 339 in two, one an SM.
+    const uint32_t least = grad ? 2 : 3;
+    uint32_t ctas = kMostCtas, fit = 2;
     double best = 0.0;
     for (uint32_t c = 1; c <= kMostCtas; ++c) {
         const uint32_t bytes = 16 * (chunk_of(vecs, c) + 8) + 6 * 1024;
-        const uint32_t n = kSmemOfSm / bytes;
-        const double fill = (double)(n < 4 ? n : 4) * bytes / (1.0 + 0.05 * c);
-        if (n >= 2 && fill > best) {
+        const uint32_t n = kSmemOfSm / bytes < 4 ? kSmemOfSm / bytes : 4;
+        const double fill = (double)(n * bytes) / (1.0 + (grad && !top ? 0.1 : 0.05) * (c - 1));
+        if (n >= least && fill > best) {
             best = fill;
             ctas = c;
+            fit = n;
         }
         if (n >= 4)
             break;
     }
-    if (rows <= 2 * sms && vecs > 512) {
-        // few rows: over as many SMs as there are
-        while (ctas < kMostCtas && rows * ctas * 2 <= 2 * sms && chunk_of(vecs, ctas) > 512)
-            ctas = ctas <= 2 ? 2 * ctas : ctas <= 4 ? 8 : 8;
+    if (rows <= 4 * sms) {
+        // Few rows: over as many SMs as there are, in pieces of 4,096 logits at least.  64 rows
+        // of 50,257: 7.4 us with 2 CTAs a row, 8.5 with one, 9.4 with four; 7 rows: 6.3 with 8,
+        // 8.5 with one.
+        while (2 * ctas <= kMostCtas && 2 * ctas * rows <= sms && chunk_of(vecs, ctas) > 512)
+            ctas *= 2;
         const uint32_t chunk = chunk_of(vecs, ctas);
-        return Layout{chunk <= 512 ? 128u : chunk <= 1024 ? 256u : 512u, ctas};
+        return Layout{vecs <= 64 ? 32u : chunk <= 512 ? 128u : ctas > 1 ? 256u : 512u, ctas};
     }
-    if (rows <= 2 * sms)
-        return Layout{vecs <= 64 ? 32u : 128u, 1};
-    return Layout{vecs <= 512 ? 32u : vecs <= 1024 ? 128u : 256u, ctas};
+    // Many rows: the fewer threads, the less a row costs besides its elements, as long as
+    // shared memory is full of rows.  Rows of 2,000 logits: 158 us with one warp each, 280 with
+    // four (100,000 of them, gradient); of 8,000: 257 with 4, 340 with 8; of 16,000: 255 with
+    // 8, 290 with 4.  With two CTAs an SM 512 threads each: of 50,257 521, 541 with 256; of
+    // 100,000 262 and 272.  Rows that are only read: of 100,000 112 with 128, 116 with 256.
+    return Layout{vecs <= 512 ? 32u : vecs <= 1024 || !grad ? 128u : fit == 2 && !top ? 512u : 256u, ctas};
 }
 
 template <int DT, int OP, bool GRAD, bool TOP, int DUAL, int NT>
@@ -1079,6 +1096,8 @@ cudaError_t launch_shape(const LossArgs& a, uint32_t ctas, uint32_t sms, void* s
     if (ctas == 1) {
         const uint32_t fit = kSmemOfSm / (uint32_t)(smem + kSmemOfCta + 512 + 128 * kRecord<DUAL != 0, TOP> + (TOP ? 4096 : 0));
         clusters = sms * (fit < kResident<NT> ? fit : kResident<NT>);
+    } else if (a.rows * ctas <= 2 * sms) {
+        clusters = a.rows;   // one a cluster; they need not all run at once
     } else {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas);
@@ -1106,7 +1125,7 @@ cudaError_t launch_type(const LossArgs& a, void* stream)
     const uint32_t sms = (uint32_t)sm_count();
     if (!sms)
         return cudaErrorInvalidDevice;
-    const Layout l = layout_of((a.vocab + 7) / 8, a.rows, sms);
+    const Layout l = layout_of((a.vocab + 7) / 8, a.rows, sms, OP != kLogp, TOP);
     switch (l.threads) {
     case 32: return launch_shape<DT, OP, GRAD, TOP, DUAL, 32>(a, l.ctas, sms, stream);
     case 128: return launch_shape<DT, OP, GRAD, TOP, DUAL, 128>(a, l.ctas, sms, stream);
