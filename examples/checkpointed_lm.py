@@ -5,7 +5,7 @@
 Two emulated data-parallel ranks share one flat 16-bit parameter buffer (the
 gathered buffer of ``DataParallelStep``).  For its micro-batch each rank runs
 
-    embedding lookup -> residual blocks -> norm -> tied output layer
+    embedding lookup -> residual blocks -> norm -> tied output layer -> loss
 
 and writes its gradient, matrix after matrix, straight into its contribution
 row, which the optimizer step then reduces.  (A row holds one shard every
@@ -114,14 +114,16 @@ def loss_and_grads(s: Shapes, params: torch.Tensor, row: torch.Tensor, tokens: t
         x = torch.nn.functional.silu(u) @ p(f"down{k}").t()
         kept.append((normed, rstd, hidden))              # y, u and h are not kept
         del y, u
-    logits = (y @ p("table").t()).float()
-    loss = torch.nn.functional.cross_entropy(logits, targets)
+    logits = like(s.vocab)
+    logits.copy_(y @ p("table").t())
+
+    # the loss of every token, and the mean's gradient in the logits' place
+    losses = torch.empty(t, device="cuda")
+    z.zero_distill_loss(z.mat(logits), None, None, 1.0, 0.0, z.ids(targets), 1.0, None, 1.0 / t, losses, z.mat(logits),
+                        stream=st)
+    loss, d_logits = losses.mean(), logits
 
     # backward: the output layer, whose weight is the table
-    soft = torch.softmax(logits, 1)
-    soft[torch.arange(t, device="cuda"), targets] -= 1
-    d_logits = like(s.vocab)
-    d_logits.copy_(soft / t)
     z.zero_act_weight_grad(z.mat(d_logits), z.act8(*normed), p("gain_out"), False, g("table"), *ws.args, stream=st)
     d_y, d_h = d_logits @ p("table"), like(d)
     z.zero_norm_backward(z.mat(d_y), z.act8(*normed), rstd, p("gain_out"), None, z.mat(d_h),

@@ -197,6 +197,8 @@ zero_status_t zero_act_weight_grad(const zero_mat_t* dy, const zero_act8_t* x, c
  *     the sum of the losses times `scale` (finite), every row of it written.  It may
  *     be logits itself (same base and pitch), and NULL where only the loss is wanted.
  *   - fp32 vectors have one element a row and are 4-byte aligned.
+ *   - Where several CTAs share a row their waits for each other are bounded (4 s);
+ *     should one ever run out, the row's loss and gradient are NaN.
  *   - The target is left out of the sum that 1 - p[target] is taken from, so that
  *     loss and gradient keep their relative precision where p is almost 1. */
 #define ZERO_LOSS_MAX_VOCAB 393216u

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const LossArgs a)
             return;
         uint32_t lo = 0, hi = 2 * a.pairs + 1;   // the first start behind the row
         while (lo < hi) {
-            const uint32_t mid = (lo + hi) / 2;
+            const uint32_t mid = lo + (hi - lo) / 2;
             if (load_id(a.starts, a.start_bytes, mid) <= (int64_t)row)
                 lo = mid + 1;
             else

@@ -596,7 +596,7 @@ struct Record {
     }
 };
 
-constexpr uint64_t kWaitLimit = 1000000000ull;   // of a wait for the cluster's other CTAs, in ns
+constexpr uint64_t kWaitLimit = 4000000000ull;   // of a wait for the cluster's other CTAs, in ns
 
 // Slots of shared memory for a piece of `chunk` vectors.
 template <int NT>
@@ -873,6 +873,9 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                     mine_of.store(q + R * warp);
                 __syncthreads();
             } else {
+                // d_logits may be the logits: the others may write the target's gradient over its logit
+                // as soon as they have this CTA's sums, so the load must be back (the shuffle reads it)
+                x_raw = __shfl_sync(0xFFFFFFFFu, x_raw, 0);
                 if (lane < ctas)
                     mine_of.send(in_cta(q + R * (rank * W + warp), lane), in_cta(&bars[odd], lane));
                 ok = !failed && mbar_wait(smem_u32(&bars[odd]), phase >> odd & 1, kWaitLimit);
@@ -1096,7 +1099,7 @@ cudaError_t launch_shape(const LossArgs& a, uint32_t ctas, uint32_t sms, void* s
     if (ctas == 1) {
         const uint32_t fit = kSmemOfSm / (uint32_t)(smem + kSmemOfCta + 512 + 128 * kRecord<DUAL != 0, TOP> + (TOP ? 4096 : 0));
         clusters = sms * (fit < kResident<NT> ? fit : kResident<NT>);
-    } else if (a.rows * ctas <= 2 * sms) {
+    } else if ((uint64_t)a.rows * ctas <= 2 * sms) {
         clusters = a.rows;   // one a cluster; they need not all run at once
     } else {
         cudaLaunchConfig_t cfg = {};
