@@ -470,7 +470,9 @@ __device__ __forceinline__ F2 wide2(uint32_t w)
 // which the warps of all the cluster's CTAs give each other their sums.
 struct RowShape {
     uint32_t ctas;      // of a cluster
-    uint32_t chunk;     // vectors of 8 logits a CTA
+    uint32_t chunk;     // vectors of 8 logits a CTA, a multiple of 8
+    uint32_t sent;      // bytes of sums that the cluster sends a CTA a row
+    uint64_t wait_ns;   // of a wait for them, at most
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -595,8 +597,6 @@ struct Record {
                          : "memory");
     }
 };
-
-constexpr uint64_t kWaitLimit = 4000000000ull;   // of a wait for the cluster's other CTAs, in ns
 
 // Slots of shared memory for a piece of `chunk` vectors.
 template <int NT>
@@ -760,8 +760,8 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                 entry_x_raw[i] = load_half(z + (own ? entry[i] : 0), own, 0);
             }
         }
-        if (ctas > 1 && tid == 0)
-            mbar_arrive_expect_tx(smem_u32(&bars[odd]), 4 * R * W * ctas);
+        if (ctas > 1 && tid == 0 && !failed)
+            mbar_arrive_expect_tx(smem_u32(&bars[odd]), shape.sent);
         asm volatile("cp.async.wait_all;" ::: "memory");
         // what is no logit, and the target, which its own sum leaves out, count as -inf
         constexpr uint32_t kTwo = (uint32_t)kMinusInf<DT> << 16 | kMinusInf<DT>;
@@ -876,9 +876,11 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                 // d_logits may be the logits: the others may write the target's gradient over its logit
                 // as soon as they have this CTA's sums, so the load must be back (the shuffle reads it)
                 x_raw = __shfl_sync(0xFFFFFFFFu, x_raw, 0);
-                if (lane < ctas)
+                if (lane < ctas && !failed)
                     mine_of.send(in_cta(q + R * (rank * W + warp), lane), in_cta(&bars[odd], lane));
-                ok = !failed && mbar_wait(smem_u32(&bars[odd]), phase >> odd & 1, kWaitLimit);
+                // Once a wait has run out this CTA neither waits nor sends any more, and its rows
+                // are NaN; the others' waits then run out too.
+                ok = __all_sync(0xFFFFFFFFu, !failed && mbar_wait(smem_u32(&bars[odd]), phase >> odd & 1, shape.wait_ns));
                 phase ^= 1u << odd;
                 failed |= !ok;
             }
@@ -1029,8 +1031,11 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
         __syncthreads();
         store_late();
     }
-    if (ctas > 1)
+    if (ctas > 1) {
         cluster_barrier();   // none leaves before all have what it sends
+        if (failed)
+            __nanosleep(100000);   // nor while something it did not wait for may be on its way
+    }
 }
 
 // -- launches -------------------------------------------------------------------------------
@@ -1085,15 +1090,33 @@ Layout layout_of(uint32_t vecs, uint32_t rows, uint32_t sms, bool grad, bool top
     return Layout{vecs <= 512 ? 32u : vecs <= 1024 || !grad ? 128u : fit == 2 && !top ? 512u : 256u, ctas};
 }
 
+constexpr uint64_t kWaitLimit = 4000000000ull;   // of a wait for the cluster's other CTAs, in ns
+
+template <bool TOP, int DUAL, int NT>
+RowShape shape_of(const LossArgs& a, uint32_t ctas)
+{
+    RowShape sh;
+    sh.ctas = ctas;
+    sh.chunk = chunk_of((a.vocab + 7) / 8, ctas);
+    sh.sent = 4 * kRecord<DUAL != 0, TOP> * (NT / 32) * ctas;
+    sh.wait_ns = kWaitLimit;
+    return sh;
+}
+
+// A CTA's piece of a row, and the sums of two rows.
+template <int NT>
+size_t smem_of(const RowShape& sh)
+{
+    return 16 * (size_t)slots_of<NT>(sh.chunk) + 2 * (size_t)sh.sent;
+}
+
 template <int DT, int OP, bool GRAD, bool TOP, int DUAL, int NT>
 cudaError_t launch_shape(const LossArgs& a, uint32_t ctas, uint32_t sms, void* stream)
 {
     static std::atomic<uint64_t> allowed{0};
     const auto kernel = k_loss_rows<DT, OP, GRAD, TOP, DUAL, NT>;
-    RowShape sh;
-    sh.ctas = ctas;
-    sh.chunk = chunk_of((a.vocab + 7) / 8, ctas);
-    const size_t smem = 16 * (size_t)slots_of<NT>(sh.chunk) + 2 * 4 * kRecord<DUAL != 0, TOP> * ctas * (NT / 32);
+    const RowShape sh = shape_of<TOP, DUAL, NT>(a, ctas);
+    const size_t smem = smem_of<NT>(sh);
     allow_smem(kernel, kMostSmem, allowed);
     uint32_t clusters = 0;
     if (ctas == 1) {
