@@ -8,12 +8,11 @@ roundings (e = 2^-24, the unit roundoff of fp32; u of the 16-bit type):
     multiply-add once, each e times the exponent y log2(e) with y the distance
     to the largest logit over T, so 2 |y| e of the value; the hardware's 2^x is
     within 2^-22 = 4 e: (2 |y| + 4) e together;
-  - a sum of n exponentials: a lane adds at most n / 256 + 8 of them one after
-    another (e each, for n up to a few hundred thousand and 256 lanes at least),
-    at most n / 4096 + 21 partial sums are joined on any way from a lane to the
-    result, each with two exponentials and three roundings (11 e); the
-    exponentials' own errors average to at most (2 log n + 4) e, log n <= 13:
-    below (n / 256 + n / 372 + 300) e, for which (n / 128 + 300) e stands;
+  - a sum of n exponentials: a lane adds at most n / 128 + 136 of them one after another (rows
+    of up to 4,096 have 32 lanes, others 128 at least), e each; a dozen partial sums at most
+    are joined on any way from a lane to the result, each with an exponential and two
+    roundings (6 e); the exponentials' own errors average to at most (2 log n + 4) e, log n <=
+    13: below (n / 128 + 136 + 72 + 30) e, for which (n / 128 + 300) e stands;
   - lse = c ln 2 + log s: the sum's relative error, k's rounding (e |m / T|) and
     four roundings of the parts;
   - lp below -log 2: the sum's error and 2^-21 of the parts; above it lp =

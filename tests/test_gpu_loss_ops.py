@@ -224,6 +224,65 @@ def test_masks_and_special_rows(dtype):
     assert bool(torch.isnan(d.t[3:].float()).any(1).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [60, 5000])
+def test_masks_of_a_low_value(dtype, vocab):
+    """Masks of the type's lowest value and of others that no logit comes near.  Rows that they leave nothing of: uniform
+    within 2^30 log 2 = 7.4e8 of zero, NaN beyond, where they count as -inf."""
+    low = torch.finfo(TYPES[dtype]).min
+    g, x, targets = batch(23, 12, vocab, dtype, pad=0.0)
+    targets[:] = torch.arange(12, device=DEV)
+    x[0, 12:] = low
+    x[1, ::2] = low
+    x[2, 12:] = -30000.0
+    x[3, :] = -30000.0
+    x[4, :] = 60000.0
+    x[5, :] = low
+    x[5, 5] = 1.0
+    x[6, 20:] = max(-1e10, low)
+    x[7, 20:] = max(-1e20, low)
+    x[8, 20:] = max(-2e9, low)
+    x[9, :] = max(-5e8, low)
+    x[10, :] = max(-1e12, low)
+    x[11, :] = low
+    gone = [10, 11] if dtype == "bf16" else []
+    kept = [i for i in range(12) if i not in gone]
+    y = Banded(len(kept), vocab, x.dtype, x[kept]).t
+    t = targets[kept].contiguous()
+    check_logprob(y, t, 1.0)
+    one = torch.ones(len(kept), device=DEV)
+    d = grad_of(y)
+    z.zero_token_logprob_backward(z.mat(y), z.ids(t), 1.0, one, z.mat(d.t))
+    near(d.t, ref.logprob_backward(y, t, 1.0, one, dtype), "d_logits")
+    # a teacher's entries on masked logits: an infinite loss where those count as -inf, so not of these rows
+    near_ones = [i for i in range(12) if bool((x[i].double().abs() < 7e8).all())]
+    y = Banded(len(near_ones), vocab, x.dtype, x[near_ones]).t
+    top, ids = teacher(g, y, 5)
+    check_distill(y, top, ids, 2.0, 0.5, targets[near_ones].contiguous(), 0.5, None, 1.0, dtype)
+    if gone:
+        lp, d = torch.empty(12, device=DEV), grad_of(x)
+        z.zero_token_logprob(z.mat(x), z.ids(targets), 1.0, lp)
+        z.zero_token_logprob_backward(z.mat(x), z.ids(targets), 1.0, torch.ones(12, device=DEV), z.mat(d.t))
+        assert bool(torch.isnan(lp[gone]).all()) and bool(torch.isfinite(lp[kept]).all())
+        assert bool(torch.isnan(d.t[gone].float()).any(1).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_far_from_zero(dtype):
+    """Rows whose logits are all large, where only differences count."""
+    g = gen(29)
+    x = torch.randn(6, 700, generator=g, device=DEV) * 300
+    x += torch.tensor([60000.0, -60000.0, 20000.0, -3000.0, 1000.0, 0.0], device=DEV)[:, None]
+    x = Banded(6, 700, TYPES[dtype], x).t
+    t = torch.arange(6, device=DEV)
+    one = torch.ones(6, device=DEV)
+    for temp in (1.0, 100.0):
+        check_logprob(x, t, temp)
+        d = grad_of(x)
+        z.zero_token_logprob_backward(z.mat(x), z.ids(t), temp, one, z.mat(d.t))
+        near(d.t, ref.logprob_backward(x, t, temp, one, dtype), "d_logits")
+
+
 def test_targets_beyond_the_vocabulary():
     g, x, targets = batch(4, 50, 300, "bf16", pad=0.0)
     targets[::7] = 300

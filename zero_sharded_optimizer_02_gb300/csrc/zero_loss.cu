@@ -132,6 +132,8 @@ zero_status_t check_rows(const zero_mat_t* logits, const zero_ids_t* targets, co
     constexpr double log2e = 1.4426950408889634;
     split(log2e / (double)temperature, a.k, a.k_low);
     split(log2e, a.k1, a.k1_low);
+    a.skew = a.k_low / a.k;
+    a.skew1 = a.k1_low / a.k1;
     a.temperature = temperature;
     a.scale = scale;
     return ZERO_OK;
@@ -310,6 +312,7 @@ extern "C" zero_status_t zero_distill_loss(const zero_mat_t* logits, const zero_
     } else {
         a.k = a.k1;   // the cross-entropy alone
         a.k_low = a.k1_low;
+        a.skew = a.skew1;
     }
     // two temperatures; of 2 and 4, one's exponentials are powers of the other's
     const int dual = !top || hard == 0.0f || temperature == 1.0f ? 0 : temperature == 2.0f ? 2 : temperature == 4.0f ? 3 : 1;

@@ -6,9 +6,9 @@
 // gradient a (p_j - [j is the target]), from which distillation takes a q_j more.
 //
 // Exponentials are taken to base 2 at x k - c, with k = log2(e) / T and c the largest
-// x k.  Every sum names the c that it is relative to, so what c was rounded by
-// cancels.  k is taken in two parts in the sums: one fp32 alone is off by up to 2^-25
-// of the distances between logits, always to the same side.  With R the sum over
+// x k, rounded up to a whole number.  Every sum names the c that it is relative to, so
+// what c was rounded by cancels.  k is taken in two parts in the sums: one fp32 alone is
+// off by up to 2^-24 of the distances between logits, always to the same side.  With R the sum over
 // all elements but the target, and e the target's own: p = e / (R + e), 1 - p =
 // R / (R + e) and log p = -log1p(R / e), which all keep their relative precision
 // however near to 1 p is.
@@ -32,6 +32,7 @@ struct LossArgs {
     uint32_t pairs;
     float k, k1;              // log2(e) / T, log2(e)
     float k_low, k1_low;      // what they lack
+    float skew, skew1;        // that over k, k1
     float temperature;
     float scale;              // of the gradient, 1 / T in it
     // inputs and outputs, one a row
@@ -67,7 +68,9 @@ constexpr float kLn2 = 0.69314712286f, kLn2Low = 5.769999045e-08f;   // ln 2 in 
 // measured on 2^20 points of each (at most 1.42e-7 on either side).  A sum of many
 // exponentials is low by as much.
 constexpr float kExpLow = 5.0e-8f;
-constexpr float kLowest = -1e30f;         // c of a sum without finite elements
+// The least c.  Beyond 2^30 a whole number of fp32 is no longer near x k; elements
+// below that count as -inf, and a row whose largest is above it as NaN.
+constexpr float kLowest = -1073741824.0f;
 
 __device__ __forceinline__ int64_t load_id(const void* ids, uint32_t bytes, uint64_t i)
 {
@@ -266,13 +269,16 @@ __device__ __forceinline__ float2 log_prob(float x, float k, float k_low, float 
 {
     if (r < e)
         return make_float2(-log1pf(r / e), 0.0f);
-    if (x == -INFINITY)   // of a row without any other logit: NaN
-        return make_float2(r > 0.0f ? -INFINITY : __uint_as_float(0x7FC00000u), 0.0f);
     const float s = r + e;
+    if (!(s > 0.0f))   // nothing to choose from
+        return make_float2(__uint_as_float(0x7FC00000u), 0.0f);
+    if (x == -INFINITY)
+        return make_float2(x, 0.0f);
     const int n = ((int)__float_as_uint(s) - 0x3F400000) >> 23;
     const float m = __uint_as_float(__float_as_uint(s) - ((uint32_t)n << 23));
-    const float p = x * k, whole = c + (float)n, d = p - whole, back = d - p;
-    const float q = fmaf(x, k_low, fmaf(x, k, -p)) + ((p - (d - back)) - (whole + back));
+    const float p = x * k, f = (float)n, d1 = p - c, back1 = d1 - p, d = d1 - f, back = d - d1;
+    const float lost = ((p - (d1 - back1)) - (c + back1)) + ((d1 - (d - back)) - (f + back));
+    const float q = fmaf(x, k_low, fmaf(x, k, -p)) + lost;
     const float h = d * kLn2;
     const float rest = (fmaf(q, kLn2, fmaf(d, kLn2Low, fmaf(d, kLn2, -h))) - low) - logf(m);
     const float v = h + rest + (s - s);   // a sum that is NaN has no m
@@ -301,7 +307,9 @@ __device__ __forceinline__ float2 policy_row(const LossArgs& a, const RowIn& in,
     return make_float2(in.d * loss, in.d * slope);
 }
 
-// A row's gradient from its sums and its target's logit (-inf if it has none).
+// A row's gradient from its sums and its target's logit (-inf if it has none).  The
+// gradient's exponentials take k without k_low; 2^(c k_low / k) makes up for that at
+// the largest logit, and near it to 2^-23 of the distance.
 template <int OP, int DUAL, bool TOP>
 __device__ __forceinline__ RowOut slopes(const LossArgs& a, const RowIn& in, const RowSums& t, float x, bool bad)
 {
@@ -319,10 +327,10 @@ __device__ __forceinline__ RowOut slopes(const LossArgs& a, const RowIn& in, con
             e1 = ex2(fmaf(x, a.k1_low, fmaf(x, a.k1, -t.s1.c)));
             r1 = t.s1.r;
             o.c1 = t.s1.c;
-            o.g = __fdividef(at_t, s);
-            o.g1 = __fdividef(at_1, r1 + e1);
+            o.g = __fdividef(at_t, s) * ex2(t.s.c * a.skew);
+            o.g1 = __fdividef(at_1, r1 + e1) * ex2(t.s1.c * a.skew1);
         } else {
-            o.g = __fdividef(at_t + at_1, s);
+            o.g = __fdividef(at_t + at_1, s) * ex2(t.s.c * a.skew);
         }
         o.at = at_t * __fdividef(e, s) - at_1 * __fdividef(r1, r1 + e1);
         return o;
@@ -331,7 +339,7 @@ __device__ __forceinline__ RowOut slopes(const LossArgs& a, const RowIn& in, con
     if (OP == kPolicy)
         slope = policy_row(a, in, log_prob(x, a.k, a.k_low, t.s.c, e, t.s.r, kExpLow).x).y;
     const float g = -(slope * a.scale);
-    o.g = __fdividef(g, s);
+    o.g = __fdividef(g, s) * ex2(t.s.c * a.skew);
     o.at = -g * __fdividef(t.s.r, s);
     return o;
 }
@@ -348,7 +356,7 @@ __device__ __forceinline__ void results(const LossArgs& a, uint32_t row, const R
             return;
         float loss = 0.0f;
         if (TOP && t.w.r != 0.0f && a.soft != 0.0f)
-            loss = a.soft * a.temperature * a.temperature *
+            loss = a.soft * a.temperature * a.temperature * (s > 0.0f ? 1.0f : __uint_as_float(0x7FC00000u)) *
                    (t.wd / t.w.r / a.temperature + kLn2 * ((t.s.c - t.w.c) + (log2f(s) - log2f(t.w.r))));
         if (a.hard != 0.0f) {
             const Sum one = DUAL ? t.s1 : t.s;
@@ -465,9 +473,11 @@ __device__ __forceinline__ F2 wide2(uint32_t w)
 // A row is held in the shared memory of a cluster of CTAs, an equal piece in each, so
 // that it is read from memory once: every thread copies its own vectors there
 // (cp.async; it waits for its own copies alone), adds up their exponentials, and turns
-// them into gradients from there.  While a row is worked on the next ones of the
-// cluster are on their way into the other buffers.  A row costs one barrier, at
-// which the warps of all the cluster's CTAs give each other their sums.
+// them into gradients from there.  As a thread is done with a vector the next row's is
+// copied into its place.  A row costs one barrier, at which the warps of all the
+// cluster's CTAs give each other their sums.  What bounds it is memory where gradients
+// are written (16,384 x 50,257: 6.3 TB/s of reads and writes) and instructions where rows
+// are only read or take two softmaxes (5.7 and 5.2 TB/s).
 struct RowShape {
     uint32_t ctas;      // of a cluster
     uint32_t chunk;     // vectors of 8 logits a CTA, a multiple of 8
@@ -525,16 +535,17 @@ template <int DT>
 constexpr uint16_t kMinusInf = DT == ZERO_F16 ? 0xFC00u : 0xFF80u;
 
 constexpr size_t kMostSmem = 215 * 1024;   // dynamic, beside the static
-constexpr uint32_t kMostCtas = 8;   // of a cluster
+constexpr uint32_t kMostCtas = 8;          // of a cluster
+
 template <int DT>
 __device__ __forceinline__ uint32_t max_of8(uint4 w)
 {
     return max2<DT>(max2<DT>(w.x, w.y), max2<DT>(w.z, w.w));
 }
 
-// CTAs an SM that the registers are divided among (64 a thread, or 1,024 threads).
+// CTAs an SM that the registers are divided among (64 a thread; 80 for a warp's rows).
 template <int NT>
-constexpr int kResident = NT == 1024 ? 1 : NT == 512 ? 2 : NT == 256 ? 4 : NT == 128 ? 8 : 24;
+constexpr int kResident = NT == 512 ? 2 : NT == 256 ? 4 : NT == 128 ? 8 : 24;
 
 // What the warps of a cluster tell each other of a row, in R floats: the sums at k,
 // at k1 (DUAL) and over the teacher's entries (TOP).
@@ -903,7 +914,7 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                 else
                     join_lanes<DUAL != 0, TOP, 32>(t);
                 if (!ok)
-                    t.s.r = t.s1.r = __uint_as_float(0x7FC00000u);
+                    t.s.r = t.s1.r = __uint_as_float(0x7FC00000u);   // unfinished
             }
         } else {
             __syncwarp();   // every lane has read what it needs of the row
@@ -921,6 +932,8 @@ __global__ void __launch_bounds__(NT, kResident<NT>) k_loss_rows(const LossArgs 
                 if (DUAL)
                     rebase(t.s1, SQ ? t.s.c * (1 << SQ) : fmaxf(t.s1.c, reference(x, a.k1)));
             }
+            if (t.s.c > -kLowest || (DUAL && t.s1.c > -kLowest))
+                t.s.r = t.s1.r = __uint_as_float(0x7FC00000u);
             if (GRAD)
                 o = slopes<OP, DUAL, TOP>(a, in, t, x, all_rows.bad);
             if (OP != kSlope && OP != kPairs && rank == 0 && warp == 0) {
